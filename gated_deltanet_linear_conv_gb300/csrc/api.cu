@@ -85,6 +85,127 @@ int check_dims(const char* fn, const gdn_dims* d, const int32_t* cu) {
   return GDN_OK;
 }
 
+// Checks of the paged-attention calls.
+int check_attn_dims(const char* fn, const gdn_attn_dims* d, const int32_t* cu) {
+  if (d == nullptr) return fail(GDN_ERR_INVALID_ARG, "%s: dims is NULL", fn);
+  if (d->num_seqs < 1) return fail(GDN_ERR_INVALID_ARG, "%s: num_seqs = %d < 1", fn, d->num_seqs);
+  if (d->total_tokens < 0) return fail(GDN_ERR_INVALID_ARG, "%s: total_tokens < 0", fn);
+  if (d->num_q_heads < 1 || d->num_kv_heads < 1)
+    return fail(GDN_ERR_INVALID_ARG, "%s: head counts must be >= 1", fn);
+  if (d->num_q_heads % d->num_kv_heads != 0)
+    return fail(GDN_ERR_INVALID_ARG, "%s: num_q_heads (%d) is not a multiple of num_kv_heads (%d)", fn,
+                d->num_q_heads, d->num_kv_heads);
+  if (d->num_q_heads > 65535) return fail(GDN_ERR_UNSUPPORTED, "%s: more than 65535 query heads", fn);
+  if (d->head_dim != 64 && d->head_dim != 128 && d->head_dim != 256)
+    return fail(GDN_ERR_UNSUPPORTED, "%s: head dim %d not in {64, 128, 256}", fn, d->head_dim);
+  if (cu == nullptr && d->total_tokens % d->num_seqs != 0)
+    return fail(GDN_ERR_INVALID_ARG, "%s: total_tokens %% num_seqs != 0 without cu_seqlens", fn);
+  OPTIONAL_PTR(cu);
+  return GDN_OK;
+}
+
+int check_heads(const char* fn, const char* name, const gdn_heads* h, int dtype) {
+  if (h == nullptr || h->data == nullptr) return fail(GDN_ERR_INVALID_ARG, "%s: %s is NULL", fn, name);
+  const int64_t unit = dtype == GDN_BF16 ? 8 : 4;
+  if (!aligned16(h->data)) return fail(GDN_ERR_INVALID_ARG, "%s: %s is not 16-byte aligned", fn, name);
+  if (h->token_stride < 0 || h->head_stride < 0 || h->token_stride % unit != 0 || h->head_stride % unit != 0)
+    return fail(GDN_ERR_INVALID_ARG, "%s: the strides of %s must be multiples of 16 bytes, >= 0", fn, name);
+  return GDN_OK;
+}
+
+int check_norm_rope(const char* fn, const gdn_attn_dims* d, const gdn_norm_rope* nr) {
+  OPTIONAL_PTR(nr->q_norm_w);
+  OPTIONAL_PTR(nr->k_norm_w);
+  OPTIONAL_PTR(nr->positions);
+  if (nr->rotary_dim < 0 || nr->rotary_dim > d->head_dim)
+    return fail(GDN_ERR_INVALID_ARG, "%s: rotary_dim %d not in [0, head_dim]", fn, nr->rotary_dim);
+  if (nr->rotary_dim % 16 != 0)
+    return fail(GDN_ERR_UNSUPPORTED, "%s: rotary_dim %d is not a multiple of 16", fn, nr->rotary_dim);
+  if (nr->rotary_dim > 0) {
+    const float* cos_sin = nr->cos_sin;
+    REQUIRE_PTR(cos_sin);
+    if (nr->max_positions < 1) return fail(GDN_ERR_INVALID_ARG, "%s: max_positions < 1", fn);
+    if (nr->interleaved != 0 && nr->interleaved != 1)
+      return fail(GDN_ERR_INVALID_ARG, "%s: interleaved must be 0 or 1", fn);
+  }
+  return GDN_OK;
+}
+
+int check_cache(const char* fn, const gdn_attn_dims* d, const gdn_paged_cache* c, int dtype) {
+  if (c == nullptr) return fail(GDN_ERR_INVALID_ARG, "%s: cache is NULL", fn);
+  const void *cache_k = c->k, *cache_v = c->v;
+  const int32_t *block_table = c->block_table, *kv_lens = c->kv_lens;
+  REQUIRE_PTR(cache_k);
+  REQUIRE_PTR(cache_v);
+  REQUIRE_PTR(block_table);
+  REQUIRE_PTR(kv_lens);
+  if (c->num_pages < 1 || c->page_size < 1 || c->max_pages < 1)
+    return fail(GDN_ERR_INVALID_ARG, "%s: num_pages, page_size and max_pages must be >= 1", fn);
+  const int64_t unit = dtype == GDN_BF16 ? 8 : 4, most = (int64_t)1 << (dtype == GDN_BF16 ? 39 : 38);
+  const int64_t st[3] = {c->page_stride, c->head_stride, c->slot_stride};
+  for (int i = 0; i < 3; ++i)
+    if (st[i] <= 0 || st[i] % unit != 0 || st[i] >= most)
+      return fail(GDN_ERR_INVALID_ARG, "%s: the cache strides must be positive multiples of 16 bytes below 2^40 bytes",
+                  fn);
+  if (c->slot_stride < d->head_dim)
+    return fail(GDN_ERR_INVALID_ARG, "%s: the cache's slot_stride is below head_dim", fn);
+  return GDN_OK;
+}
+
+gdn::HeadsIn heads_in(const gdn_heads* h) {
+  return h == nullptr ? gdn::HeadsIn{nullptr, 0, 0} : gdn::HeadsIn{h->data, h->token_stride, h->head_stride};
+}
+
+gdn::PagedCache paged_cache(const gdn_paged_cache* c) {
+  return {c->k, c->v, c->page_stride, c->head_stride, c->slot_stride, c->block_table, c->kv_lens,
+          c->num_pages, c->page_size, c->max_pages};
+}
+
+#define CHECK(call)                   \
+  do {                                \
+    const int st_ = (call);           \
+    if (st_ != GDN_OK) return st_;    \
+  } while (0)
+
+// The part common to gdn_qk_norm_rope and gdn_paged_kv_append (cache null: dense k_out).
+int norm_rope(const char* fn, const gdn_attn_dims* dims, const int32_t* cu, const gdn_heads* q, const gdn_heads* k,
+              const gdn_heads* v, int in_dtype, const gdn_norm_rope* nr, const gdn_paged_cache* cache, int kv_dtype,
+              void* q_out, int q_dtype, void* k_out, void* stream) {
+  CHECK(check_attn_dims(fn, dims, cu));
+  if (!valid_dtype(in_dtype) || !valid_dtype(kv_dtype) || !valid_dtype(q_dtype))
+    return fail(GDN_ERR_INVALID_ARG, "%s: bad dtype", fn);
+  if (nr != nullptr) CHECK(check_norm_rope(fn, dims, nr));
+  if (dims->total_tokens == 0) return GDN_OK;
+  if (q != nullptr) {
+    CHECK(check_heads(fn, "q", q, in_dtype));
+    REQUIRE_PTR(q_out);
+  }
+  if (k != nullptr) CHECK(check_heads(fn, "k", k, in_dtype));
+  if (v != nullptr) CHECK(check_heads(fn, "v", v, in_dtype));
+  if (cache != nullptr) CHECK(check_cache(fn, dims, cache, kv_dtype));
+  else if (k != nullptr) REQUIRE_PTR(k_out);
+  int* flag = nullptr;
+  CHECK(get_flag(&flag));
+  gdn::NormRopeArgs p{};
+  p.q = heads_in(q); p.k = heads_in(k); p.v = heads_in(v);
+  p.q_out = q_out; p.k_out = k_out;
+  if (cache != nullptr) p.c = paged_cache(cache);
+  if (nr != nullptr) {
+    p.qw = nr->q_norm_w; p.kw = nr->k_norm_w; p.eps = nr->norm_eps;
+    p.rot = nr->rotary_dim; p.inter = nr->interleaved; p.max_pos = nr->max_positions;
+    p.table = nr->cos_sin; p.pos = nr->positions;
+  }
+  p.cu = cu; p.num_seqs = dims->num_seqs; p.total = dims->total_tokens;
+  p.Nq = q != nullptr ? dims->num_q_heads : 0;
+  p.Nkv = k != nullptr ? dims->num_kv_heads : 0;
+  p.D = dims->head_dim;
+  p.in_bf16 = in_dtype == GDN_BF16; p.q_bf16 = q_dtype == GDN_BF16; p.kv_bf16 = kv_dtype == GDN_BF16;
+  p.err = flag;
+  cudaError_t e = gdn::launch_norm_rope(p, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, fn);
+  return GDN_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -108,7 +229,10 @@ int gdn_check_device_error(void* stream) {
     e = cudaMemcpy(flag, &zero, sizeof(int), cudaMemcpyHostToDevice);
     if (e != cudaSuccess) return cuda_fail(e, "clear device error flag");
     return fail(GDN_ERR_DEVICE, "device error %d (%s)", host,
-                host == 1 ? "inconsistent cu_seqlens" : host == 2 ? "bounded wait timed out" : "?");
+                host == 1   ? "inconsistent cu_seqlens"
+                : host == 2 ? "bounded wait timed out"
+                : host == 3 ? "kv_lens, a page id or a position out of range"
+                            : "?");
   }
   return GDN_OK;
 }
@@ -491,6 +615,67 @@ int gdn_decode_fused(const gdn_dims* dims, const void* mixed_qkv, int in_dtype,
   p.q_scale = q_scale; p.l2_eps = l2_eps; p.norm_eps = norm_eps;
   p.in_bf16 = in_dtype == GDN_BF16; p.out_bf16 = out_dtype == GDN_BF16;
   cudaError_t e = gdn::launch_decode_fused(p, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, fn);
+  return GDN_OK;
+}
+
+int gdn_qk_norm_rope(const gdn_attn_dims* dims, const int32_t* cu_seqlens, const gdn_heads* q,
+                     const gdn_heads* k, int in_dtype, const gdn_norm_rope* nr, void* q_out,
+                     void* k_out, int out_dtype, void* stream) {
+  const char* fn = "gdn_qk_norm_rope";
+  if (q == nullptr) return fail(GDN_ERR_INVALID_ARG, "%s: q is NULL", fn);
+  if (nr == nullptr) return fail(GDN_ERR_INVALID_ARG, "%s: nr is NULL", fn);
+  return norm_rope(fn, dims, cu_seqlens, q, k, nullptr, in_dtype, nr, nullptr, out_dtype, q_out, out_dtype, k_out,
+                   stream);
+}
+
+int gdn_paged_kv_append(const gdn_attn_dims* dims, const int32_t* cu_seqlens, const gdn_heads* q,
+                        const gdn_heads* k, const gdn_heads* v, int in_dtype,
+                        const gdn_norm_rope* nr, const gdn_paged_cache* cache, int cache_dtype,
+                        void* q_out, int q_dtype, void* stream) {
+  const char* fn = "gdn_paged_kv_append";
+  if (k == nullptr || v == nullptr) return fail(GDN_ERR_INVALID_ARG, "%s: %s is NULL", fn, k == nullptr ? "k" : "v");
+  if (cache == nullptr) return fail(GDN_ERR_INVALID_ARG, "%s: cache is NULL", fn);
+  return norm_rope(fn, dims, cu_seqlens, q, k, v, in_dtype, nr, cache, cache_dtype, q_out, q_dtype, nullptr, stream);
+}
+
+int gdn_paged_attn_decode_workspace_size(const gdn_attn_dims* dims, size_t* bytes) {
+  const char* fn = "gdn_paged_attn_decode_workspace_size";
+  if (dims == nullptr || bytes == nullptr) return fail(GDN_ERR_INVALID_ARG, "%s: NULL argument", fn);
+  gdn_attn_dims d = *dims;
+  if (d.num_seqs > 1) d.num_seqs = 1;            // the bounds come with the call: no equal split required here
+  CHECK(check_attn_dims(fn, &d, nullptr));
+  *bytes = gdn::paged_attn_workspace_bytes(dims->num_seqs, dims->total_tokens, dims->num_q_heads,
+                                           dims->num_kv_heads, dims->head_dim);
+  return GDN_OK;
+}
+
+int gdn_paged_attn_decode(const gdn_attn_dims* dims, const int32_t* cu_seqlens, const gdn_heads* q,
+                          const gdn_heads* gate, int in_dtype, const gdn_paged_cache* cache,
+                          float scale, void* o, int out_dtype, void* workspace,
+                          size_t workspace_bytes, void* stream) {
+  const char* fn = "gdn_paged_attn_decode";
+  CHECK(check_attn_dims(fn, dims, cu_seqlens));
+  if (!valid_dtype(in_dtype) || !valid_dtype(out_dtype)) return fail(GDN_ERR_INVALID_ARG, "%s: bad dtype", fn);
+  if (dims->total_tokens == 0) return GDN_OK;
+  CHECK(check_heads(fn, "q", q, in_dtype));
+  if (gate != nullptr) CHECK(check_heads(fn, "gate", gate, in_dtype));
+  CHECK(check_cache(fn, dims, cache, in_dtype));
+  REQUIRE_PTR(o);
+  const size_t need = gdn::paged_attn_workspace_bytes(dims->num_seqs, dims->total_tokens, dims->num_q_heads,
+                                                      dims->num_kv_heads, dims->head_dim);
+  if (need > 0 && (workspace == nullptr || workspace_bytes < need || !aligned16(workspace)))
+    return fail(GDN_ERR_INVALID_ARG, "%s: workspace of %zu bytes (16-byte aligned) required, got %zu", fn, need,
+                workspace_bytes);
+  int* flag = nullptr;
+  CHECK(get_flag(&flag));
+  gdn::PagedAttnArgs p{};
+  p.q = heads_in(q); p.gate = heads_in(gate); p.c = paged_cache(cache); p.o = o;
+  p.cu = cu_seqlens; p.num_seqs = dims->num_seqs; p.total = dims->total_tokens;
+  p.Nq = dims->num_q_heads; p.Nkv = dims->num_kv_heads; p.D = dims->head_dim;
+  p.scale = scale; p.in_bf16 = in_dtype == GDN_BF16; p.out_bf16 = out_dtype == GDN_BF16;
+  p.ws = workspace; p.err = flag;
+  cudaError_t e = gdn::launch_paged_attn(p, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, fn);
   return GDN_OK;
 }

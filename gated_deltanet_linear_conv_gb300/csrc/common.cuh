@@ -32,6 +32,7 @@ enum DeviceError : int {
   kDevErrNone = 0,
   kDevErrSeqlens = 1,   // cu_seqlens not monotone / out of [0, total_tokens]
   kDevErrTimeout = 2,   // a bounded wait on an mbarrier ran out
+  kDevErrCache = 3,     // kv_lens, a page id or a position out of its range
 };
 
 __device__ __forceinline__ void raise_error(int* flag, int code) {
@@ -153,6 +154,16 @@ __device__ __forceinline__ bool seq_bounds(const int32_t* cu, int num_seqs, int 
                   (s + 1 < num_seqs || eos == total);
   if (!ok) bos = eos = 0;
   return ok;
+}
+
+// Raises the error flag for a cu_seqlens with an inconsistent sequence: thread `i` of `n`
+// looks at every n-th one.
+__device__ __forceinline__ void check_seqs(const int32_t* cu, int num_seqs, int total, int64_t i, int64_t n, int* err) {
+  if (cu == nullptr) return;
+  for (int64_t s = i; s < num_seqs; s += n) {
+    int bos, eos;
+    if (!seq_bounds(cu, num_seqs, total, (int)s, bos, eos)) raise_error(err, kDevErrSeqlens);
+  }
 }
 
 }  // namespace gdn

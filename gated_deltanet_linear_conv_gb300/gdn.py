@@ -24,13 +24,39 @@ EXPORTS = ('gdn_version', 'gdn_last_error_string', 'gdn_check_device_error', 'gd
            'gdn_gating', 'gdn_chunk_prefill_workspace_size', 'gdn_chunk_prefill',
            'gdn_chunk_prefill_fp32', 'gdn_chunk_prefill_static', 'gdn_chunk_prefill_gated_norm',
            'gdn_recurrent_decode', 'gdn_recurrent_decode_steps',
-           'gdn_gated_rmsnorm', 'gdn_decode_fused', 'gdn_test_chunk_wait_timeout')
+           'gdn_gated_rmsnorm', 'gdn_decode_fused',
+           'gdn_qk_norm_rope', 'gdn_paged_kv_append', 'gdn_paged_attn_decode_workspace_size',
+           'gdn_paged_attn_decode', 'gdn_test_chunk_wait_timeout')
 
 
 class gdn_dims(ctypes.Structure):
     _fields_ = [('num_seqs', ctypes.c_int32), ('total_tokens', ctypes.c_int32),
                 ('num_k_heads', ctypes.c_int32), ('num_v_heads', ctypes.c_int32),
                 ('head_k_dim', ctypes.c_int32), ('head_v_dim', ctypes.c_int32)]
+
+
+class gdn_attn_dims(ctypes.Structure):
+    _fields_ = [('num_seqs', ctypes.c_int32), ('total_tokens', ctypes.c_int32),
+                ('num_q_heads', ctypes.c_int32), ('num_kv_heads', ctypes.c_int32),
+                ('head_dim', ctypes.c_int32)]
+
+
+class gdn_heads(ctypes.Structure):
+    _fields_ = [('data', ctypes.c_void_p), ('token_stride', ctypes.c_int64), ('head_stride', ctypes.c_int64)]
+
+
+class gdn_norm_rope(ctypes.Structure):
+    _fields_ = [('q_norm_w', ctypes.c_void_p), ('k_norm_w', ctypes.c_void_p), ('norm_eps', ctypes.c_float),
+                ('rotary_dim', ctypes.c_int32), ('interleaved', ctypes.c_int32),
+                ('max_positions', ctypes.c_int32), ('cos_sin', ctypes.c_void_p),
+                ('positions', ctypes.c_void_p)]
+
+
+class gdn_paged_cache(ctypes.Structure):
+    _fields_ = [('k', ctypes.c_void_p), ('v', ctypes.c_void_p), ('page_stride', ctypes.c_int64),
+                ('head_stride', ctypes.c_int64), ('slot_stride', ctypes.c_int64),
+                ('num_pages', ctypes.c_int32), ('page_size', ctypes.c_int32), ('max_pages', ctypes.c_int32),
+                ('block_table', ctypes.c_void_p), ('kv_lens', ctypes.c_void_p)]
 
 
 _lib = None
@@ -40,6 +66,10 @@ _F = ctypes.c_float
 _I64 = ctypes.c_int64
 _SZ = ctypes.c_size_t
 _DIMS = ctypes.POINTER(gdn_dims)
+_ADIMS = ctypes.POINTER(gdn_attn_dims)
+_HEADS = ctypes.POINTER(gdn_heads)
+_NR = ctypes.POINTER(gdn_norm_rope)
+_CACHE = ctypes.POINTER(gdn_paged_cache)
 
 _SIGS = {
     'gdn_version': ([], _I),
@@ -60,6 +90,10 @@ _SIGS = {
     'gdn_gated_rmsnorm': ([_I64, ctypes.c_int32, _P, _I, _P, _I, _P, _F, _P, _I, _P], _I),
     'gdn_decode_fused': ([_DIMS, _P, _I, _P, _P, _P, _P, _P, _P, _P, _F, _F, _P, _P, _P, _F,
                           _P, _I, _P], _I),
+    'gdn_qk_norm_rope': ([_ADIMS, _P, _HEADS, _HEADS, _I, _NR, _P, _P, _I, _P], _I),
+    'gdn_paged_kv_append': ([_ADIMS, _P, _HEADS, _HEADS, _HEADS, _I, _NR, _CACHE, _I, _P, _I, _P], _I),
+    'gdn_paged_attn_decode_workspace_size': ([_ADIMS, ctypes.POINTER(_SZ)], _I),
+    'gdn_paged_attn_decode': ([_ADIMS, _P, _HEADS, _HEADS, _I, _CACHE, _F, _P, _I, _P, _SZ, _P], _I),
     'gdn_test_chunk_wait_timeout': ([_DIMS, _P, _P, _P, _P, _P, _P, _P, _SZ, _I64, _P], _I),
 }
 
@@ -343,3 +377,181 @@ def mixer_prefill(mixed_qkv, conv_w, a, b, A_log, dt_bias, z, norm_w, Nk, Nv, Dk
                          act_dtype, bufs.get('o'), bufs.get('workspace'))
     y = gated_rmsnorm(o, z, norm_w, norm_eps, out_dtype, bufs.get('y'))
     return y, S
+
+
+# --- softmax attention over a paged cache ---------------------------------------------
+
+def _same_device(*tensors):
+    """The library launches on the current device: every tensor has to live there."""
+    for t in tensors:
+        if t is not None and (not t.is_cuda or t.device.index != torch.cuda.current_device()):
+            raise ValueError('expected CUDA tensors on the current device')
+
+
+def _heads(t, what):
+    """[tokens, heads, D] with contiguous head rows (a slice of a wider projection is fine)."""
+    if t is None:
+        return None
+    if t.dim() != 3:
+        raise ValueError('%s must be [tokens, heads, head_dim]' % what)
+    (T, H, D), (ts, hs, es) = t.shape, t.stride()
+    if es != 1:
+        raise ValueError('the head rows of %s must be contiguous' % what)
+    # a stride over an axis of one entry is never used: any value may stand there
+    return gdn_heads(t.data_ptr(), ts if T > 1 else H * D, hs if H > 1 else D)
+
+
+def _int32(t, what):
+    if t is not None and t.dtype != torch.int32:
+        raise ValueError('%s must be int32' % what)
+    return t
+
+
+def _norm_rope(q_norm_w, k_norm_w, norm_eps, cos_sin, positions, interleaved, T, D):
+    rot = 0
+    if cos_sin is not None:
+        if cos_sin.dim() != 2:
+            raise ValueError('cos_sin must be [positions, rotary_dim]')
+        rot = cos_sin.shape[1]
+    for w in (q_norm_w, k_norm_w):
+        if w is not None and w.numel() != D:
+            raise ValueError('a norm weight has head_dim elements')
+    if positions is not None and positions.numel() != T:
+        raise ValueError('positions has one entry per token')
+    return gdn_norm_rope(_ptr(_f32(q_norm_w)), _ptr(_f32(k_norm_w)), norm_eps, rot, 1 if interleaved else 0,
+                         cos_sin.shape[0] if rot else 0, _ptr(_f32(cos_sin)), _ptr(_int32(positions, 'positions')))
+
+
+def _cache(k_cache, v_cache, block_table, kv_lens, Nkv, D, num_seqs):
+    """Checks the cache's tensors against the call's sizes and packs them."""
+    if k_cache.dim() != 4 or k_cache.shape != v_cache.shape or k_cache.dtype != v_cache.dtype:
+        raise ValueError('k_cache and v_cache share the shape [pages, kv heads, page size, head_dim] and a dtype')
+    pages, H, P, E = k_cache.shape
+    if H != Nkv or E != D:
+        raise ValueError('the cache holds %d heads of %d, the call has %d of %d' % (H, E, Nkv, D))
+
+    def strides(t):
+        ps, hs, ss, es = t.stride()
+        if es != 1:
+            raise ValueError('the head rows of the cache must be contiguous')
+        # a stride over an axis of one entry is never used: any value may stand there
+        return (ps if pages > 1 else H * P * E, hs if H > 1 else P * E, ss if P > 1 else E)
+
+    ps, hs, ss = strides(k_cache)
+    if strides(v_cache) != (ps, hs, ss):
+        raise ValueError('k_cache and v_cache must have the same strides')
+    if block_table.dim() != 2 or block_table.shape[0] != num_seqs or kv_lens.numel() != num_seqs:
+        raise ValueError('block_table is [sequences, pages] and kv_lens [sequences]')
+    return gdn_paged_cache(k_cache.data_ptr(), v_cache.data_ptr(), ps, hs, ss, pages, P, block_table.shape[1],
+                           _ptr(_int32(block_table, 'block_table')), _ptr(_int32(kv_lens, 'kv_lens')))
+
+
+def _out(t, shape, dtype, device, what):
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if t.shape != torch.Size(shape):
+        raise ValueError('%s must have the shape %s' % (what, tuple(shape)))
+    return t
+
+
+def qk_norm_rope(q, k=None, cos_sin=None, q_norm_w=None, k_norm_w=None, positions=None, cu_seqlens=None,
+                 num_seqs=1, norm_eps=1e-6, interleaved=False, out_dtype=torch.bfloat16, q_out=None, k_out=None):
+    """gdn_qk_norm_rope: per-head RMSNorm and rotation of q [tokens, Nq, D] and k [tokens, Nkv, D].
+    Returns (q_out, k_out); ``positions`` default to each token's index in its sequence."""
+    T, Nq, D = q.shape
+    Nkv = k.shape[1] if k is not None else Nq
+    if k is not None and (k.shape != (T, Nkv, D) or k.dtype != q.dtype):
+        raise ValueError('q and k share tokens, head_dim and dtype')
+    _same_device(q, k, cos_sin, q_norm_w, k_norm_w, positions, cu_seqlens, q_out, k_out)
+    if cu_seqlens is not None:
+        num_seqs = _int32(cu_seqlens, 'cu_seqlens').numel() - 1
+    q_out = _out(q_out, (T, Nq, D), out_dtype, q.device, 'q_out')
+    if k is not None:
+        k_out = _out(k_out, (T, Nkv, D), q_out.dtype, q.device, 'k_out')
+        if k_out.dtype != q_out.dtype:
+            raise ValueError('q_out and k_out share a dtype')
+    d = gdn_attn_dims(num_seqs, T, Nq, Nkv, D)
+    nr = _norm_rope(q_norm_w, k_norm_w, norm_eps, cos_sin, positions, interleaved, T, D)
+    st = lib().gdn_qk_norm_rope(d, _ptr(cu_seqlens), _heads(q, 'q'), _heads(k, 'k'), _dt(q), nr, _ptr(q_out),
+                                _ptr(k_out) if k is not None else None, _dt(q_out), _stream())
+    _check(st, 'gdn_qk_norm_rope')
+    return q_out, k_out
+
+
+def paged_kv_append(k, v, k_cache, v_cache, block_table, kv_lens, q=None, cos_sin=None, q_norm_w=None,
+                    k_norm_w=None, positions=None, cu_seqlens=None, norm_eps=1e-6, interleaved=False,
+                    out_dtype=torch.bfloat16, q_out=None):
+    """gdn_paged_kv_append: k (normed and rotated on the way) and v of the new tokens into the cache, in place.
+    k_cache, v_cache are [pages, Nkv, page size, D] (a [pages, page size, Nkv, D] cache goes in transposed);
+    kv_lens include the new tokens.  Returns the normed and rotated q (None without q)."""
+    T, Nkv, D = k.shape
+    if v.shape != k.shape or v.dtype != k.dtype:
+        raise ValueError('k and v share a shape and a dtype')
+    Nq = Nkv
+    if q is not None:
+        Nq = q.shape[1]
+        if q.shape != (T, Nq, D) or q.dtype != k.dtype:
+            raise ValueError('q shares tokens, head_dim and dtype with k')
+    _same_device(k, v, k_cache, v_cache, block_table, kv_lens, q, cos_sin, q_norm_w, k_norm_w, positions,
+                 cu_seqlens, q_out)
+    num_seqs = kv_lens.numel()
+    if cu_seqlens is not None and _int32(cu_seqlens, 'cu_seqlens').numel() != num_seqs + 1:
+        raise ValueError('cu_seqlens has one entry more than kv_lens')
+    c = _cache(k_cache, v_cache, block_table, kv_lens, Nkv, D, num_seqs)
+    if q is not None:
+        q_out = _out(q_out, (T, Nq, D), out_dtype, q.device, 'q_out')
+    d = gdn_attn_dims(num_seqs, T, Nq, Nkv, D)
+    nr = _norm_rope(q_norm_w, k_norm_w, norm_eps, cos_sin, positions, interleaved, T, D)
+    st = lib().gdn_paged_kv_append(d, _ptr(cu_seqlens), _heads(q, 'q'), _heads(k, 'k'), _heads(v, 'v'), _dt(k), nr, c,
+                                   _dt(k_cache), _ptr(q_out) if q is not None else None,
+                                   _dt(q_out) if q is not None else GDN_BF16, _stream())
+    _check(st, 'gdn_paged_kv_append')
+    return q_out if q is not None else None
+
+
+def paged_attn_decode_workspace_size(num_seqs, total, Nq, Nkv, D):
+    n = _SZ(0)
+    _check(lib().gdn_paged_attn_decode_workspace_size(gdn_attn_dims(num_seqs, total, Nq, Nkv, D), n),
+           'gdn_paged_attn_decode_workspace_size')
+    return n.value
+
+
+def paged_attn_decode(q, k_cache, v_cache, block_table, kv_lens, scale=None, gate=None, cu_seqlens=None,
+                      out_dtype=torch.bfloat16, o=None, workspace=None):
+    """gdn_paged_attn_decode: attention of the new tokens q [tokens, Nq, D] (one or a few per sequence, bounds
+    from cu_seqlens, else equally many) over the cache, times sigmoid(gate) when given.  Returns o."""
+    T, Nq, D = q.shape
+    if k_cache.dtype != q.dtype or (gate is not None and (gate.dtype != q.dtype or gate.shape != q.shape)):
+        raise ValueError('q, gate and the cache share a dtype; gate has the shape of q')
+    _same_device(q, k_cache, v_cache, block_table, kv_lens, gate, cu_seqlens, o, workspace)
+    num_seqs = kv_lens.numel()
+    if cu_seqlens is not None and _int32(cu_seqlens, 'cu_seqlens').numel() != num_seqs + 1:
+        raise ValueError('cu_seqlens has one entry more than kv_lens')
+    Nkv = k_cache.shape[1]
+    c = _cache(k_cache, v_cache, block_table, kv_lens, Nkv, D, num_seqs)
+    o = _out(o, (T, Nq, D), out_dtype, q.device, 'o')
+    ws_bytes = paged_attn_decode_workspace_size(num_seqs, T, Nq, Nkv, D)
+    if workspace is None and ws_bytes > 0:
+        workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=q.device)
+    d = gdn_attn_dims(num_seqs, T, Nq, Nkv, D)
+    st = lib().gdn_paged_attn_decode(d, _ptr(cu_seqlens), _heads(q, 'q'), _heads(gate, 'gate'), _dt(q), c,
+                                     1.0 / math.sqrt(D) if scale is None else scale, _ptr(o), _dt(o),
+                                     _ptr(workspace), workspace.numel() * workspace.element_size()
+                                     if workspace is not None else 0, _stream())
+    _check(st, 'gdn_paged_attn_decode')
+    return o
+
+
+def attention_decode(q, k, v, k_cache, v_cache, block_table, kv_lens, cos_sin=None, q_norm_w=None, k_norm_w=None,
+                     gate=None, positions=None, cu_seqlens=None, scale=None, norm_eps=1e-6, interleaved=False,
+                     out_dtype=torch.bfloat16, bufs=None):
+    """One step of a full-attention layer from its projections to the input of its output projection, the
+    counterpart of decode_fused in a hybrid decoder's other layers: paged_kv_append (k and v into the cache, q
+    and k normed and rotated) -> paged_attn_decode (with the output gate).
+
+    ``bufs`` (optional dict) supplies preallocated q, o, workspace."""
+    bufs = bufs or {}
+    qr = paged_kv_append(k, v, k_cache, v_cache, block_table, kv_lens, q, cos_sin, q_norm_w, k_norm_w, positions,
+                         cu_seqlens, norm_eps, interleaved, k_cache.dtype, bufs.get('q'))
+    return paged_attn_decode(qr, k_cache, v_cache, block_table, kv_lens, scale, gate, cu_seqlens, out_dtype,
+                             bufs.get('o'), bufs.get('workspace'))

@@ -29,9 +29,10 @@
  *    errors are detected on the host before any launch.  A launch failure
  *    returns GDN_ERR_CUDA; gdn_last_error_string() describes the last error
  *    of the calling thread.  Inconsistent device-side metadata (a cu_seqlens
- *    that is not monotone or does not end at total_tokens) is detected on the
- *    device: the offending kernel skips the bad sequence and raises a sticky
- *    device error flag, read (and cleared) by gdn_check_device_error().
+ *    that is not monotone or does not end at total_tokens; see gdn_paged_cache
+ *    for the cache's) is detected on the device: the offending kernel skips the
+ *    bad sequence and raises a sticky device error flag, read (and cleared) by
+ *    gdn_check_device_error().
  *  - On its first use on a device the library looks up (once, with that device
  *    current) the device addresses of its own module variables: the error
  *    flag and the scratch array of gdn_chunk_prefill_static.  Those addresses
@@ -39,8 +40,8 @@
  *    (cudaDeviceReset) or destroying its primary context after the first call
  *    is not supported: later calls would use stale addresses.
  *
- * Supported sizes: Dk, Dv in {64, 128}; Nv a multiple of Nk; conv kernel 4;
- * chunk 64.  Other sizes return GDN_ERR_UNSUPPORTED.
+ * Supported sizes of the mixer: Dk, Dv in {64, 128}; Nv a multiple of Nk; conv
+ * kernel 4; chunk 64.  Other sizes return GDN_ERR_UNSUPPORTED.
  */
 #ifndef GDN_H_
 #define GDN_H_
@@ -357,6 +358,159 @@ int gdn_decode_fused(const gdn_dims* dims,
                      float q_scale, float l2_eps,
                      float* state, const void* z, const float* norm_w, float norm_eps,
                      void* y, int out_dtype, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Softmax attention over a paged cache: the serving calls for the
+ * full-attention layers that a hybrid decoder interleaves with the mixer
+ * ([QDA], the full-attention layers: RMSNorm of q and k per head, partial
+ * rotation, grouped query heads, sigmoid output gate; section "Cache": keys and
+ * values kept per position).  Query head h reads key/value head h / (Nq / Nkv).
+ *
+ *   gdn_qk_norm_rope        norm + rotation of q and k, dense outputs
+ *   gdn_paged_kv_append     norm + rotation of q and k, k and v into the cache
+ *   gdn_paged_attn_decode   attention of the new tokens over the cache
+ *
+ * Head sizes 64, 128 and 256 (else GDN_ERR_UNSUPPORTED).
+ * ------------------------------------------------------------------------ */
+
+/* Sizes: N sequences, total_tokens new tokens over all of them (bounds from
+ * cu_seqlens as above), Nq query heads, a multiple of Nkv, head size D. */
+typedef struct {
+  int32_t num_seqs;
+  int32_t total_tokens;
+  int32_t num_q_heads;
+  int32_t num_kv_heads;
+  int32_t head_dim;
+} gdn_attn_dims;
+
+/* An input [tokens, heads, D] whose head rows are contiguous: element
+ * (t, h, i) is data[t * token_stride + h * head_stride + i].  Strides are in
+ * elements, >= 0 and multiples of 16 bytes, so that q, k, v or a gate can be a
+ * slice of a joint projection output. */
+typedef struct {
+  const void* data;
+  int64_t token_stride;
+  int64_t head_stride;
+} gdn_heads;
+
+/* Per-head RMSNorm and rotation of q and k, computed in float32 and rounded
+ * once when stored.
+ *   q_norm_w, k_norm_w  [D] float32, or NULL (that one is not normalised):
+ *                       u = x / sqrt(mean(x^2) + norm_eps) * w
+ *                       (a layer that defines its weight as 1 + w passes 1 + w)
+ *   cos_sin             [max_positions, rotary_dim] float32: row p holds the
+ *                       rotary_dim / 2 cosines of position p, then its sines
+ *                       (made by the caller, in float64 for far positions);
+ *                       NULL when rotary_dim = 0 (no rotation)
+ *   rotary_dim          r: the first r elements of a head are rotated, the
+ *                       others pass; a multiple of 16, at most D
+ *   interleaved         0: element i is paired with i + r/2;  1: 2i with 2i+1
+ *                       (a, b) -> (a cos_i - b sin_i, b cos_i + a sin_i)
+ *   positions           [tokens] int32 table rows, or NULL: the token's index
+ *                       in its sequence (gdn_qk_norm_rope) or its index in the
+ *                       cache (gdn_paged_kv_append)
+ * A position outside [0, max_positions) raises the device error flag, and
+ * nothing is written for its token. */
+typedef struct {
+  const float* q_norm_w;
+  const float* k_norm_w;
+  float norm_eps;
+  int32_t rotary_dim;
+  int32_t interleaved;
+  int32_t max_positions;
+  const float* cos_sin;
+  const int32_t* positions;
+} gdn_norm_rope;
+
+/* A paged key/value cache.  Element i of slot j of key/value head h in page p
+ * is at p * page_stride + h * head_stride + j * slot_stride + i of k and of v
+ * (strides in elements, positive multiples of 16 bytes, below 2^40 bytes;
+ * slot_stride >= D), so both a [pages, Nkv, page_size, D] and a
+ * [pages, page_size, Nkv, D] cache, or the two halves of a
+ * [pages, 2, ...] one, can be passed.
+ *   block_table  [N, max_pages] int32: index p of sequence s lives in slot
+ *                p % page_size of page block_table[s, p / page_size]; entries
+ *                past a sequence's length are not read
+ *   kv_lens      [N] int32: the sequence's cached tokens INCLUDING the call's
+ *                new ones: new token i of n has cache index kv_lens[s] - n + i.
+ *                0 marks an inactive slot of a padded batch.
+ * A length below 0, below the sequence's new tokens (unless 0) or above
+ * max_pages * page_size, and a page id outside [0, num_pages), raise the
+ * device error flag. */
+typedef struct {
+  void* k;
+  void* v;
+  int64_t page_stride;
+  int64_t head_stride;
+  int64_t slot_stride;
+  int32_t num_pages;
+  int32_t page_size;
+  int32_t max_pages;
+  const int32_t* block_table;
+  const int32_t* kv_lens;
+} gdn_paged_cache;
+
+/* ------------------------------------------------------------------------
+ * gdn_qk_norm_rope -- per-head norm and rotation of queries and keys.
+ *   q [tokens, Nq, D], k [tokens, Nkv, D]   in_dtype (strided, see gdn_heads);
+ *                                           k may be NULL (q alone)
+ *   q_out [tokens, Nq, D], k_out [tokens, Nkv, D]   out_dtype, contiguous;
+ *       may be the input's own memory when that is contiguous and of the same
+ *       type, and must not overlap an input otherwise
+ * ------------------------------------------------------------------------ */
+int gdn_qk_norm_rope(const gdn_attn_dims* dims, const int32_t* cu_seqlens,
+                     const gdn_heads* q, const gdn_heads* k, int in_dtype,
+                     const gdn_norm_rope* nr,
+                     void* q_out, void* k_out, int out_dtype, void* stream);
+
+/* ------------------------------------------------------------------------
+ * gdn_paged_kv_append -- writes the new tokens' keys (normed and rotated on
+ * the way) and values into the cache, and norms and rotates q beside them.
+ *   q              NULL: only k and v;  else q_out [tokens, Nq, D] q_dtype,
+ *                  contiguous (may be q's own memory, as above)
+ *   k, v           [tokens, Nkv, D]   in_dtype (strided)
+ *   nr             NULL: neither norm nor rotation
+ *   cache          written in cache_dtype; read: block_table and kv_lens
+ * Nothing is written for an inactive sequence (kv_lens = 0; q_out neither) nor
+ * for a token whose metadata raised the error flag.  Two tokens that map to
+ * one slot leave either one's values there.
+ * ------------------------------------------------------------------------ */
+int gdn_paged_kv_append(const gdn_attn_dims* dims, const int32_t* cu_seqlens,
+                        const gdn_heads* q, const gdn_heads* k, const gdn_heads* v,
+                        int in_dtype, const gdn_norm_rope* nr,
+                        const gdn_paged_cache* cache, int cache_dtype,
+                        void* q_out, int q_dtype, void* stream);
+
+/* ------------------------------------------------------------------------
+ * gdn_paged_attn_decode -- attention of the new tokens of each sequence over
+ * its cache (whose last entries are the new tokens' own, appended before):
+ *   o[t, h] = sum_j softmax_j(scale * q[t, h] . k_j) v_j   over the cache
+ *             indices j up to the token's own
+ *   y[t, h] = o[t, h] * sigmoid(gate[t, h])                when gate is given
+ * Rows of an inactive sequence (kv_lens = 0) and of one whose kv_lens raised
+ * the error flag are zero; a page id that raised it reads as zeros.  Cache
+ * entries past a token's own index never reach its row, whatever they hold.
+ * Scores, softmax statistics and sums are float32.
+ *
+ * Made for one or a few new tokens per sequence (decode, draft + verify):
+ * every 8 (token, query head) rows of a key/value head are one tile of the
+ * products, a few tiles share one pass over the cache, and a sequence with
+ * more new tokens takes more passes.
+ *
+ *   q, gate    [tokens, Nq, D]   in_dtype (strided); gate may be NULL
+ *   cache      in_dtype
+ *   o          [tokens, Nq, D]   out_dtype, contiguous
+ *   workspace  device scratch of gdn_paged_attn_decode_workspace_size() bytes
+ *              (may be NULL when that is 0), no initialisation needed; not to
+ *              be shared by calls that can run at the same time
+ * ------------------------------------------------------------------------ */
+int gdn_paged_attn_decode_workspace_size(const gdn_attn_dims* dims, size_t* bytes);
+
+int gdn_paged_attn_decode(const gdn_attn_dims* dims, const int32_t* cu_seqlens,
+                          const gdn_heads* q, const gdn_heads* gate, int in_dtype,
+                          const gdn_paged_cache* cache, float scale,
+                          void* o, int out_dtype,
+                          void* workspace, size_t workspace_bytes, void* stream);
 
 /* ------------------------------------------------------------------------
  * Test hook (no counterpart on the source pages): failure detection of the
