@@ -531,3 +531,25 @@ def test_sequences_that_share_pages():
     c.bt[1, :2] = c.bt[0, :2]
     c.block_table = i32(c.bt)
     check_attn(c, rand(96, 2, 8, 64), [40, 45], [1, 1])
+
+
+@pytest.mark.parametrize('D,H,dtype', [(256, 2, BF), (128, 2, BF), (64, 2, BF), (256, 1, F32), (128, 1, F32)])
+def test_long_contexts_back_to_back(D, H, dtype):
+    """Many calls in flight on two caches, warps running ahead of one another over long ranges: every output is
+    the first one's, bit for bit, and the first is right."""
+    n = 131072 if dtype == BF else 30000
+    cs = [Cache([n], H, 64, D, dtype, seed=s) for s in (1, 2)]
+    for s, c in enumerate(cs):
+        g = torch.Generator(device='cuda').manual_seed(s)
+        c.k.normal_(generator=g)
+        c.v.normal_(generator=g)
+    q = rand(1, 1, 8 * H, D, dtype=dtype)
+    first = [check_attn(c, q, [n], [1], out_dtype=dtype, cu=False) for c in cs]
+    outs = [run_attn_async(c, q, n, dtype) for _ in range(100) for c in cs]
+    gdn.check_device_error()
+    for i, y in enumerate(outs):
+        assert torch.equal(y, first[i % 2]), i
+
+
+def run_attn_async(c, q, n, dtype):
+    return gdn.paged_attn_decode(q, c.k, c.v, c.block_table, i32([n]), out_dtype=dtype)
