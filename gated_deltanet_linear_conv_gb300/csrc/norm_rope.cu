@@ -15,81 +15,132 @@
 namespace gdn {
 namespace {
 
-template <typename Tin, typename Tq, typename Tkv, int D, bool CACHE>
-__global__ void __launch_bounds__(256)
-norm_rope_kernel(NormRopeArgs p) {
-  constexpr int LPR = D / 8;                       // lanes per row
-  constexpr int RPW = 32 / LPR;                    // rows per warp
-  const int lane = threadIdx.x & 31;
-  const int c = lane % LPR;                        // this lane's 8-element chunk of its row
-  const int rows_per_token = p.Nq + (CACHE ? 2 : 1) * p.Nkv;
-  const int64_t rows = (int64_t)p.total * rows_per_token;
-  const int64_t step = (int64_t)gridDim.x * (blockDim.x >> 5) * RPW;
-  const int64_t first = ((int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5)) * RPW;
-  check_seqs(p.cu, p.num_seqs, p.total, (int64_t)blockIdx.x * blockDim.x + threadIdx.x,
-             (int64_t)gridDim.x * blockDim.x, p.err);
-  for (int64_t r0 = first; r0 < rows; r0 += step) {
-    const int64_t row = r0 + lane / LPR;
-    const bool live = row < rows;
-    const int t = live ? (int)(row / rows_per_token) : 0;
-    const int h = live ? (int)(row % rows_per_token) : 0;
-    const bool is_q = h < p.Nq, is_v = h >= p.Nq + p.Nkv;
-    const HeadsIn in = is_q ? p.q : is_v ? p.v : p.k;
-    const int hh = is_q ? h : is_v ? h - p.Nq - p.Nkv : h - p.Nq;
+// Eight consecutive elements as loaded.
+template <typename T> struct Chunk;
+template <> struct Chunk<bf16> {
+  uint4 u;
+  __device__ __forceinline__ void load(const bf16* p) { u = *reinterpret_cast<const uint4*>(p); }
+  __device__ __forceinline__ void get(float (&f)[8]) const {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 v = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w[i]));
+      f[2 * i] = v.x;
+      f[2 * i + 1] = v.y;
+    }
+  }
+};
+template <> struct Chunk<float> {
+  float4 a, b;
+  __device__ __forceinline__ void load(const float* p) {
+    a = *reinterpret_cast<const float4*>(p);
+    b = *reinterpret_cast<const float4*>(p + 4);
+  }
+  __device__ __forceinline__ void get(float (&f)[8]) const {
+    f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w; f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+  }
+};
 
-    // where the token stands: its sequence, its index there and in the cache
+constexpr int kThreads = 128;
+constexpr int kRows = 4;                           // rows of a token that a lane group holds at once
+
+// A group of D/8 lanes takes kRows consecutive rows (q heads, then k heads, then v heads) of
+// one token: their loads go out together and first, the token's metadata and its table
+// entries, read once for all of them, behind.  Block x: tokens, block y: rows.
+template <typename Tin, typename Tq, typename Tkv, int D, bool CACHE>
+__global__ void __launch_bounds__(kThreads)
+norm_rope_kernel(const __grid_constant__ NormRopeArgs p) {
+  constexpr int LPR = D / 8;                       // lanes per row
+  const int c = threadIdx.x % LPR;                 // this lane's 8-element chunk of its rows
+  const int t = blockIdx.x * (kThreads / LPR) + threadIdx.x / LPR;
+  const int h0 = blockIdx.y * kRows;
+  const int rows = p.Nq + (CACHE ? 2 : 1) * p.Nkv;
+  const bool live = t < p.total;
+  const int lane = threadIdx.x & 31;
+
+  Chunk<Tin> raw[kRows];
+#pragma unroll
+  for (int u = 0; u < kRows; ++u) {
+    const int h = h0 + u;
+    if (live && h < rows) {
+      const HeadsIn& in = h < p.Nq ? p.q : h < p.Nq + p.Nkv ? p.k : p.v;
+      const int hh = h < p.Nq ? h : h < p.Nq + p.Nkv ? h - p.Nq : h - p.Nq - p.Nkv;
+      raw[u].load(static_cast<const Tin*>(in.p) + t * in.ts + hh * in.hs + c * 8);
+    }
+  }
+  // where the token stands: its sequence, its index there and in the cache
+  if (blockIdx.y == 0) check_seqs(p.cu, p.num_seqs, p.total, (int64_t)blockIdx.x * kThreads + threadIdx.x,
+                                  (int64_t)gridDim.x * kThreads, p.err);
+  bool ok = live;
+  int pos = 0, page = 0, slot = 0;
+  if (CACHE || (p.rot > 0 && p.pos == nullptr) || p.cu != nullptr) {
     const int s = find_seq(p.cu, p.num_seqs, p.total, t);
-    int bos = 0, eos = 0, err = 0;
-    bool ok = live && seq_bounds(p.cu, p.num_seqs, p.total, s, bos, eos) && t >= bos && t < eos;
-    int pos = t - bos, page = 0, slot = 0;
+    int bos = 0, eos = 0;
+    ok = ok && seq_bounds(p.cu, p.num_seqs, p.total, s, bos, eos) && t >= bos && t < eos;
+    pos = t - bos;
     if (CACHE && ok) {
+      bool bad = false;
       const int len = __ldg(p.c.lens + s);
       if (len == 0) {
         ok = false;                                // an inactive sequence: nothing to write
       } else if (len < eos - bos || (int64_t)len > (int64_t)p.c.max_pages * p.c.page_size) {
-        err = kDevErrCache;
-        ok = false;
+        bad = true;
       } else {
         pos = len - (eos - bos) + (t - bos);
         page = __ldg(p.c.bt + (int64_t)s * p.c.max_pages + pos / p.c.page_size);
         slot = pos % p.c.page_size;
-        if (page < 0 || page >= p.c.num_pages) {
-          err = kDevErrCache;
-          ok = false;
-        }
+        bad = page < 0 || page >= p.c.num_pages;
       }
-    }
-    if (p.rot > 0 && ok) {
-      if (p.pos != nullptr) pos = __ldg(p.pos + t);
-      if (pos < 0 || pos >= p.max_pos) {
-        err = kDevErrCache;
+      if (bad) {
         ok = false;
+        if (c == 0) raise_error(p.err, kDevErrCache);
       }
     }
-    if (live && err != 0 && c == 0) raise_error(p.err, err);
-
-    float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    if (ok) load8(static_cast<const Tin*>(in.p) + t * in.ts + hh * in.hs + c * 8, x);
-    const float* w = is_v ? nullptr : is_q ? p.qw : p.kw;
-    float ss = 0.f;
+  }
+  if (p.rot > 0 && ok) {
+    if (p.pos != nullptr) pos = __ldg(p.pos + t);
+    if (pos < 0 || pos >= p.max_pos) {
+      ok = false;
+      if (c == 0) raise_error(p.err, kDevErrCache);
+    }
+  }
+  // this lane's cosines and sines: 8 of each half-split, 4 interleaved
+  const int half = p.rot / 16;                     // chunks in half of the rotated part
+  const bool turn = c * 8 < p.rot;
+  const bool low = c < half;
+  const int partner = lane - c + (turn ? (low ? c + half : c - half) : c);
+  float co[8], si[8];
+  if (turn && ok && h0 < p.Nq + p.Nkv) {
+    const float* cs = p.table + (int64_t)pos * p.rot;
+    if (p.inter) {
+      load4(cs + c * 4, *reinterpret_cast<float(*)[4]>(co));
+      load4(cs + p.rot / 2 + c * 4, *reinterpret_cast<float(*)[4]>(si));
+    } else {
+      load8(cs + (low ? c : c - half) * 8, co);
+      load8(cs + p.rot / 2 + (low ? c : c - half) * 8, si);
+    }
+  }
 #pragma unroll
-    for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
-    ss = group_sum(ss, LPR);
+  for (int u = 0; u < kRows; ++u) {
+    const int h = h0 + u;
+    if (h >= rows) break;                          // (the same for the whole block)
+    const bool is_q = h < p.Nq, is_v = h >= p.Nq + p.Nkv;
+    float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    if (live) raw[u].get(x);
+    const float* w = is_v ? nullptr : is_q ? p.qw : p.kw;
     if (w != nullptr) {
-      const float inv = rsqrtf(ss * (1.0f / D) + p.eps);
-      float wf[8];
+      float ss = 0.f, wf[8];
       load8(w + c * 8, wf);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
+      ss = group_sum(ss, LPR);
+      const float inv = rsqrtf(ss * (1.0f / D) + p.eps);
 #pragma unroll
       for (int i = 0; i < 8; ++i) x[i] = x[i] * inv * wf[i];
     }
-    if (p.rot > 0) {
-      const float* cs = p.table + (ok ? (int64_t)pos * p.rot : 0);
-      const bool turn = ok && !is_v && c * 8 < p.rot;
+    if (p.rot > 0 && !is_v) {
       if (p.inter) {
         if (turn) {
-          float co[4], si[4];
-          load4(cs + c * 4, co);
-          load4(cs + p.rot / 2 + c * 4, si);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const float a = x[2 * i], b = x[2 * i + 1];
@@ -98,17 +149,10 @@ norm_rope_kernel(NormRopeArgs p) {
           }
         }
       } else {
-        const int half = p.rot / 16;               // chunks in half of the rotated part
-        const bool low = c < half;
-        const int partner = lane - c + (c * 8 < p.rot ? (low ? c + half : c - half) : c);
         float y[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) y[i] = __shfl_sync(0xffffffffu, x[i], partner);
         if (turn) {
-          const int at = (low ? c : c - half) * 8;
-          float co[8], si[8];
-          load8(cs + at, co);
-          load8(cs + p.rot / 2 + at, si);
 #pragma unroll
           for (int i = 0; i < 8; ++i) x[i] = x[i] * co[i] + (low ? -y[i] : y[i]) * si[i];
         }
@@ -116,12 +160,13 @@ norm_rope_kernel(NormRopeArgs p) {
     }
     if (!ok) continue;
     if (is_q) {
-      store8(static_cast<Tq*>(p.q_out) + ((int64_t)t * p.Nq + hh) * D + c * 8, x);
+      store8(static_cast<Tq*>(p.q_out) + ((int64_t)t * p.Nq + h) * D + c * 8, x);
     } else if (CACHE) {
+      const int hh = is_v ? h - p.Nq - p.Nkv : h - p.Nq;
       Tkv* dst = static_cast<Tkv*>(is_v ? p.c.v : p.c.k);
       store8(dst + page * p.c.ps + hh * p.c.hs + slot * p.c.ss + c * 8, x);
     } else {
-      store8(static_cast<Tkv*>(p.k_out) + ((int64_t)t * p.Nkv + hh) * D + c * 8, x);
+      store8(static_cast<Tkv*>(p.k_out) + ((int64_t)t * p.Nkv + h - p.Nq) * D + c * 8, x);
     }
   }
 }
@@ -129,13 +174,12 @@ norm_rope_kernel(NormRopeArgs p) {
 template <typename Tin, typename Tq, typename Tkv, int D>
 cudaError_t launch_d(const NormRopeArgs& p, cudaStream_t s) {
   const bool cache = p.k_out == nullptr && p.v.p != nullptr;
-  const int64_t rows = (int64_t)p.total * (p.Nq + (cache ? 2 : 1) * p.Nkv);
-  const int rows_per_block = 8 * 32 / (D / 8);
-  const int64_t need = (rows + rows_per_block - 1) / rows_per_block;
-  const int blocks = (int)std::min<int64_t>(need, (int64_t)num_sms() * 8);
-  if (blocks == 0) return cudaSuccess;
-  if (cache) norm_rope_kernel<Tin, Tq, Tkv, D, true><<<blocks, 256, 0, s>>>(p);
-  else norm_rope_kernel<Tin, Tq, Tkv, D, false><<<blocks, 256, 0, s>>>(p);
+  const int rows = p.Nq + (cache ? 2 : 1) * p.Nkv;
+  if (p.total == 0 || rows == 0) return cudaSuccess;
+  const int per_block = kThreads / (D / 8);
+  const dim3 grid((p.total + per_block - 1) / per_block, (rows + kRows - 1) / kRows);
+  if (cache) norm_rope_kernel<Tin, Tq, Tkv, D, true><<<grid, kThreads, 0, s>>>(p);
+  else norm_rope_kernel<Tin, Tq, Tkv, D, false><<<grid, kThreads, 0, s>>>(p);
   return cudaGetLastError();
 }
 
