@@ -40,6 +40,7 @@ namespace {
 constexpr int kStageHalf = 16384;                  // bytes of K (and of V) in a stage
 constexpr int kAlignTiles = 8;                     // no unit longer than this: ranges end at unit borders
 constexpr int kMinTiles = 2;                       // tiles of a range at least (fewer CTAs for little work)
+constexpr int kMaxCtas = 256;                      // CTAs, and so pieces of a unit, at most
 constexpr uint64_t kWaitNs = 2000000000ull;        // bound of every wait
 constexpr uint32_t kPollCap = 1u << 28;
 constexpr float kLog2e = 1.4426950408889634f;
@@ -50,27 +51,29 @@ struct Cfg {
   static constexpr bool BF = sizeof(T) == 2;
   static constexpr int NT = NT_;                                   // octets per pass
   static constexpr int ROWS = NT * 8;
-  static constexpr int CW = BF ? 4 : 8;                            // consumer warps
+  static constexpr int CW = 8;                                     // consumer warps
+  static constexpr int DS = BF && D == 256 ? 2 : 1;                // warps that share a slice, each with D / DS of its output
+  static constexpr int TG = CW / DS;                               // slices in work at a time
   static constexpr int THREADS = (CW + 1) * 32;
   static constexpr int TILE = kStageHalf / (D * (int)sizeof(T));   // tokens per stage
   static constexpr int SLICE = BF ? 16 : 4;                        // tokens per warp step
   static constexpr int SL = TILE / SLICE;                          // slices per stage
-  static constexpr int USERS = SL < CW ? SL : CW;                  // warps that read a stage
+  static constexpr int USERS = SL < TG ? SL : TG;                  // slices of a stage in work at a time
   static constexpr int QPITCH = D * (int)sizeof(T) + 16;           // bytes; padded: ldmatrix without conflicts
   static constexpr int QBYTES = ROWS * QPITCH;
   static constexpr int JP = D + 4;                                 // join row pitch (floats)
-  static constexpr int JOIN = CW * 8 * JP * 4 + CW * 8 * 2 * 4;
+  static constexpr int JOIN = TG * 8 * JP * 4 + TG * 8 * 2 * 4;
   static constexpr int HEAD = 1024;
   static constexpr int FIXED = HEAD + 2 * QBYTES + JOIN;
   static constexpr int MOST = 227 * 1024 - 1024;                   // 1024: alignment of the ring
   // Where a stage has fewer slices than there are warps, GROUPS sets of warps take the stages
   // in turn; the ring is a multiple of them, so that a stage always has the same readers (a
   // warp two rounds ahead of another's would take a phase that is still to come for done).
-  static constexpr int GROUPS = CW / USERS;
+  static constexpr int GROUPS = TG / USERS;
   static constexpr int FIT = (MOST - FIXED) / (2 * kStageHalf) < 6 ? (MOST - FIXED) / (2 * kStageHalf) : 6;
   static constexpr int STAGES = FIT - FIT % GROUPS;
   static constexpr int SMEM = FIXED + STAGES * 2 * kStageHalf + 1024;
-  static_assert(STAGES >= 3 && CW % USERS == 0 && STAGES % GROUPS == 0, "ring");
+  static_assert(STAGES >= 3 && TG % USERS == 0 && STAGES % GROUPS == 0, "ring");
 };
 
 // One piece of a unit, from the producer to the consumers (and, unjoined, to the join kernel).
@@ -138,11 +141,11 @@ __device__ __forceinline__ void ldsm4t(uint32_t addr, uint32_t (&r)[4]) {
 }
 __device__ __forceinline__ uint32_t movm(uint32_t x) {
   uint32_t y;
-  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
   return y;
 }
 __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
@@ -201,13 +204,17 @@ template <int D, int NT>
 struct TcWarp {
   using C = Cfg<bf16, D, NT>;
   static constexpr int KS = D / 16;
+  static constexpr int OS = KS / C::DS;            // 16-row blocks of O^T that this warp holds
   static constexpr bool QREG = NT * D <= 256;      // query fragments stay in registers
-  float o[NT][KS][4];
+  static constexpr int CH = NT <= 2 ? 2 : 1;       // score accumulators: shorter chains of dependent products
+  float o[NT][OS][4];
   float m[NT][2], l[NT][2];
   uint32_t qf[QREG ? NT : 1][QREG ? KS : 1][2];
   uint32_t qaddr;
+  int d0;                                          // first of this warp's blocks
 
-  __device__ __forceinline__ void start(const uint8_t* q, int lane) {
+  __device__ __forceinline__ void start(const uint8_t* q, int share, int lane) {
+    d0 = share * OS;
     // x4: two k steps of one octet; lanes 8i..8i+7 give the rows of matrix i
     qaddr = tc::smem_u32(q) + (lane & 7) * C::QPITCH + (lane >> 3) * 16;
     if (QREG) {
@@ -226,7 +233,7 @@ struct TcWarp {
       m[nt][0] = m[nt][1] = -INFINITY;
       l[nt][0] = l[nt][1] = 0.f;
 #pragma unroll
-      for (int i = 0; i < KS; ++i)
+      for (int i = 0; i < OS; ++i)
 #pragma unroll
         for (int e = 0; e < 4; ++e) o[nt][i][e] = 0.f;
     }
@@ -236,11 +243,11 @@ struct TcWarp {
   template <typename Lim>
   __device__ __forceinline__ void slice(uint8_t* ks_, uint8_t* vs_, int j0, int tok0, int nvalid, float c, Lim lim,
                                         int lane) {
-    float s[NT][4];
+    float s[NT][4], s1[NT][4];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) s[nt][e] = 0.f;
+      for (int e = 0; e < 4; ++e) s[nt][e] = s1[nt][e] = 0.f;
     {
       const int row = j0 + (lane & 15);
       const uint32_t base = tc::smem_u32(ks_) + row * 128;
@@ -255,12 +262,12 @@ struct TcWarp {
         for (int nt = 0; nt < NT; ++nt) {
           if (QREG) {
             mma16816(s[nt], a0, qf[nt][ks][0], qf[nt][ks][1]);
-            mma16816(s[nt], a1, qf[nt][ks + 1][0], qf[nt][ks + 1][1]);
+            mma16816(CH == 2 ? s1[nt] : s[nt], a1, qf[nt][ks + 1][0], qf[nt][ks + 1][1]);
           } else {
             uint32_t r[4];
             ldsm4(qaddr + nt * 8 * C::QPITCH + ks * 32, r);
             mma16816(s[nt], a0, r[0], r[1]);
-            mma16816(s[nt], a1, r[2], r[3]);
+            mma16816(CH == 2 ? s1[nt] : s[nt], a1, r[2], r[3]);
           }
         }
       }
@@ -271,7 +278,7 @@ struct TcWarp {
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) s[nt][e] *= c;
+      for (int e = 0; e < 4; ++e) s[nt][e] = (CH == 2 ? s[nt][e] + s1[nt][e] : s[nt][e]) * c;
       if (tail) {
         const int last = lim(nt) - tok0;
         if (g >= last) s[nt][0] = s[nt][1] = -INFINITY;
@@ -294,7 +301,7 @@ struct TcWarp {
           l[nt][e] *= al[e];
         }
 #pragma unroll
-        for (int i = 0; i < KS; ++i)
+        for (int i = 0; i < OS; ++i)
 #pragma unroll
           for (int e = 0; e < 4; ++e) o[nt][i][e] *= al[e & 1];
       }
@@ -314,13 +321,14 @@ struct TcWarp {
     const int vrow = j0 + (lane & 7) + ((lane >> 4) << 3);
     const uint32_t vbase = tc::smem_u32(vs_) + vrow * 128;
     const uint32_t vsw = (uint32_t)(vrow & 7);
-    auto vfrag = [&](int i, uint32_t (&a)[4]) {
+    auto vfrag = [&](int b, uint32_t (&a)[4]) {
+      const int i = d0 + b;
       const uint32_t ch = (uint32_t)((i & 3) * 2 + ((lane >> 3) & 1));
       ldsm4t(vbase + (i >> 2) * (C::TILE * 128) + ((ch ^ vsw) << 4), a);
     };
     if (!tail) {
 #pragma unroll
-      for (int i = 0; i < KS; ++i) {
+      for (int i = 0; i < OS; ++i) {
         uint32_t a[4];
         vfrag(i, a);
 #pragma unroll
@@ -332,18 +340,18 @@ struct TcWarp {
     } else {
       // The end of the visible range: rows that an octet does not see may hold anything, and
       // 0 * NaN is NaN.  They are cleared in the stage, from the octet that sees most to the
-      // one that sees least.
+      // one that sees least; a warp clears the columns that it reads.
 #pragma unroll
       for (int nt = NT - 1; nt >= 0; --nt) {
         if (nt >= nvalid) continue;
         const int last = max(0, min(16, lim(nt) - tok0));
-        for (int e = lane; e < (16 - last) * (D / 8); e += 32) {
-          const int r = j0 + last + e / (D / 8), ch = e % (D / 8);
+        for (int e = lane; e < (16 - last) * (2 * OS); e += 32) {
+          const int r = j0 + last + e / (2 * OS), ch = 2 * d0 + e % (2 * OS);
           *reinterpret_cast<uint4*>(vs_ + (ch >> 3) * (C::TILE * 128) + r * 128 + ((ch & 7) << 4)) = make_uint4(0, 0, 0, 0);
         }
         __syncwarp();
 #pragma unroll
-        for (int i = 0; i < KS; ++i) {
+        for (int i = 0; i < OS; ++i) {
           uint32_t a[4];
           vfrag(i, a);
           mma16816(o[nt][i], a, hi[nt][0], hi[nt][1]);
@@ -363,15 +371,15 @@ struct TcWarp {
       float v = l[nt][e];
 #pragma unroll
       for (int off = 4; off < 32; off <<= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
-      if (g == 0) {
+      if (g == 0 && d0 == 0) {
         jm[2 * t + e] = m[nt][e];
         jl[2 * t + e] = v;
       }
     }
 #pragma unroll
-    for (int i = 0; i < KS; ++i)
+    for (int i = 0; i < OS; ++i)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) jo[(2 * t + (e & 1)) * C::JP + i * 16 + g + (e >> 1) * 8] = o[nt][i][e];
+      for (int e = 0; e < 4; ++e) jo[(2 * t + (e & 1)) * C::JP + (d0 + i) * 16 + g + (e >> 1) * 8] = o[nt][i][e];
   }
 };
 
@@ -401,7 +409,7 @@ struct SimtWarp {
       x[0] = f.x; x[1] = f.y;
     }
   }
-  __device__ __forceinline__ void start(const uint8_t* qs, int lane) {
+  __device__ __forceinline__ void start(const uint8_t* qs, int, int lane) {
 #pragma unroll
     for (int h = 0; h < 8; ++h) {
       row(qs + h * C::QPITCH, 0, lane, q[h]);
@@ -498,9 +506,9 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
   uint8_t* ring = tc::smem_aligned<1024>(raw);
   uint8_t* qs = ring + C::STAGES * 2 * kStageHalf;
   float* jo = reinterpret_cast<float*>(qs + 2 * C::QBYTES);
-  float* jm = jo + C::CW * 8 * C::JP;
-  float* jl = jm + C::CW * 8;
-  uint8_t* head = reinterpret_cast<uint8_t*>(jl + C::CW * 8);
+  float* jm = jo + C::TG * 8 * C::JP;
+  float* jl = jm + C::TG * 8;
+  uint8_t* head = reinterpret_cast<uint8_t*>(jl + C::TG * 8);
   uint64_t* full = reinterpret_cast<uint64_t*>(head);
   uint64_t* empty = full + C::STAGES;
   uint64_t* qfull = empty + C::STAGES;
@@ -515,7 +523,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
   if (tid == 0) {
     for (int i = 0; i < C::STAGES; ++i) {
       tc::mbar_init(full + i, 1);
-      tc::mbar_init(empty + i, C::USERS);
+      tc::mbar_init(empty + i, C::USERS * C::DS);
     }
     for (int i = 0; i < 2; ++i) {
       tc::mbar_init(qfull + i, 1);
@@ -713,6 +721,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
       }
     }
   }
+  const int tw = warp % C::TG;                     // which slices; warps tw + k TG share them
   typename WarpOf<T, D, NT>::type w;
   int it = 0;
   for (int np = 0;; ++np) {
@@ -722,11 +731,11 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
     if (ok) {
       d = piece[qslot];
       if (d.tile0 < 0) break;
-      w.start(qs + qslot * C::QBYTES, lane);
+      w.start(qs + qslot * C::QBYTES, warp / C::TG, lane);
       auto lim = [&](int nt) { return d.len - d.n + (d.x0 + min(nt, d.nvalid - 1)) / p.NG + 1; };
       const int most = lim(NT - 1);
       for (int tile = d.tile0; tile < d.tile1; ++tile, ++it) {
-        int j = C::SL >= C::CW ? warp : warp - (it * C::SL) % C::CW;       // this warp's first slice of the stage
+        int j = C::SL >= C::TG ? tw : tw - (it * C::SL) % C::TG;           // this warp's first slice of the stage
         if (j < 0 || j >= C::SL) continue;
         const int st = it % C::STAGES;
         if (!wait_bar(full + st, (it / C::STAGES) & 1, abort)) {
@@ -734,7 +743,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
           break;
         }
         uint8_t* kd = ring + st * 2 * kStageHalf;
-        for (; j < C::SL; j += C::CW) {
+        for (; j < C::SL; j += C::TG) {
           const int tok0 = tile * C::TILE + j * C::SLICE;
           if (tok0 < most) w.slice(kd, kd + kStageHalf, j * C::SLICE, tok0, d.nvalid, p.c, lim, lane);
         }
@@ -753,7 +762,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
       if (ok) {
 #pragma unroll
         for (int k = 0; k < NT; ++k)
-          if (k == nt) w.give(k, jo + warp * 8 * C::JP, jm + warp * 8, jl + warp * 8, lane);
+          if (k == nt) w.give(k, jo + tw * 8 * C::JP, jm + tw * 8, jl + tw * 8, lane);
       }
       if (tc::named_sync_or(1, C::CW * 32, !ok)) {
         quit = true;
@@ -765,10 +774,10 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
         if (oct * 8 + h >= p.G) break;
         float mt = -INFINITY, lt = 0.f, y[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int k = 0; k < C::CW; ++k) mt = fmaxf(mt, jm[k * 8 + h]);
+        for (int k = 0; k < C::TG; ++k) mt = fmaxf(mt, jm[k * 8 + h]);
         const float base = mt == -INFINITY ? 0.f : mt;
 #pragma unroll
-        for (int k = 0; k < C::CW; ++k) {
+        for (int k = 0; k < C::TG; ++k) {
           const float f = exp2f(jm[k * 8 + h] - base);
           const float4 v = *reinterpret_cast<const float4*>(jo + (k * 8 + h) * C::JP + e);
           lt = fmaf(jl[k * 8 + h], f, lt);
@@ -794,78 +803,75 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
 }
 
 // ------------------------------------------------------------------ the join
-// Block (c, y) joins rows y, y + gridDim.y, .. of the unit that starts in CTA c's range and
-// ends behind it, piece by piece in order.  Launched while the main kernel runs; its first
-// step is to wait for that kernel's end.
+// Block (c, row) joins one row of the unit that starts in CTA c's range and ends behind it,
+// its pieces in order.  All loads of a block but the record are independent: first the
+// maxima and sums (a thread per piece) for the weights, beside them the outputs, NP pieces
+// at a time.  Launched while the main kernel runs; the first step is to wait for its end.
 constexpr int kJoinThreads = 256;
 template <typename T, int D>
 __global__ void __launch_bounds__(kJoinThreads)
-paged_attn_join_kernel(const __grid_constant__ Params p, int rows_per_unit) {
+paged_attn_join_kernel(const __grid_constant__ Params p) {
   constexpr int LPR = D / 4;                       // threads across a row
   constexpr int NP = kJoinThreads / LPR;           // pieces in flight
-  __shared__ float sw[NP][LPR][4];
-  __shared__ float sl[NP], sm[NP];
+  __shared__ float sw[kMaxCtas], so[NP][D], red[2][kJoinThreads / 32];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const SplitRec r = p.rec[blockIdx.x];
-  if (!r.valid) return;
-  // pieces: CTA c's last one, then the first one of every CTA with tiles before the unit's end
-  const int c0 = blockIdx.x;
-  const int k = threadIdx.x / LPR, e = (threadIdx.x % LPR) * 4;
-  for (int row = blockIdx.y; row < r.nvalid * 8; row += gridDim.y) {
-    const int x = r.x0 + row / 8, h = (x % p.NG) * 8 + row % 8;
-    if (h >= p.G) continue;
-    float m = -INFINITY, l = 0.f, y[4] = {0.f, 0.f, 0.f, 0.f};
-    for (int c = c0 + k; c < r.geff; c += NP) {
-      const int64_t b = r.total * c / r.geff;
-      if (c > c0 && b >= r.end) break;
-      const int64_t at = ((int64_t)2 * c + (c == c0 ? 1 : 0)) * rows_per_unit + row;
-      const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + at * 2);
-      float v[4];
-      load4(p.part_o + at * D + e, v);
-      const float mn = fmaxf(m, ml.x);
-      const float base = mn == -INFINITY ? 0.f : mn;
-      const float f0 = exp2f(m - base), f1 = exp2f(ml.x - base);
-      l = l * f0 + ml.y * f1;
+  const int row = blockIdx.y, x = r.x0 + row / 8, h = (x % p.NG) * 8 + row % 8;
+  if (!r.valid || row >= r.nvalid * 8 || h >= p.G) return;
+  // CTA c0's last piece, then the first one of every CTA whose range starts before the unit's end
+  const int c0 = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int n = (int)((r.end * r.geff + r.total - 1) / r.total) - c0;
+  auto at = [&](int i) { return ((int64_t)2 * (c0 + i) + (i == 0 ? 1 : 0)) * (gridDim.y) + row; };
+  float2 ml = make_float2(-INFINITY, 0.f);
+  if (tid < n) ml = *reinterpret_cast<const float2*>(p.part_ml + at(tid) * 2);
+  float m = ml.x;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) y[i] = y[i] * f0 + v[i] * f1;
-      m = mn;
-    }
-    __syncthreads();
+  for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+  if (lane == 0) red[0][warp] = m;
+  __syncthreads();
 #pragma unroll
-    for (int i = 0; i < 4; ++i) sw[k][e / 4][i] = y[i];
-    if (e == 0) {
-      sm[k] = m;
-      sl[k] = l;
-    }
-    __syncthreads();
-    if (k == 0) {
-      float mt = -INFINITY, lt = 0.f, z[4] = {0.f, 0.f, 0.f, 0.f};
+  for (int i = 0; i < kJoinThreads / 32; ++i) m = fmaxf(m, red[0][i]);
+  const float w = exp2f(ml.x - (m == -INFINITY ? 0.f : m));
+  float l = w * ml.y;
+  if (tid < n) sw[tid] = w;
 #pragma unroll
-      for (int i = 0; i < NP; ++i) mt = fmaxf(mt, sm[i]);
-      const float base = mt == -INFINITY ? 0.f : mt;
+  for (int off = 16; off > 0; off >>= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
+  if (lane == 0) red[1][warp] = l;
+  __syncthreads();
+  l = 0.f;
 #pragma unroll
-      for (int i = 0; i < NP; ++i) {
-        const float f = exp2f(sm[i] - base);
-        lt = fmaf(sl[i], f, lt);
+  for (int i = 0; i < kJoinThreads / 32; ++i) l += red[1][i];
+  const int k = tid / LPR, e = (tid % LPR) * 4;
+  float y[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+  for (int i = k; i < n; i += NP) {
+    float v[4];
+    load4(p.part_o + at(i) * D + e, v);
+    const float f = sw[i];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) z[j] = fmaf(sw[i][e / 4][j], f, z[j]);
-      }
-      const float inv = lt == 0.f ? 0.f : 1.f / lt;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) z[j] *= inv;
-      finish4<T>(p.a, r.bos + x / p.NG, r.kvh * p.G + h, e, D, z);
-    }
+    for (int j = 0; j < 4; ++j) y[j] = fmaf(v[j], f, y[j]);
   }
+  store4(&so[k][e], y);
+  __syncthreads();
+  if (k != 0) return;
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+  for (int i = 1; i < NP; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) y[j] += so[i][e + j];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) y[j] *= inv;
+  finish4<T>(p.a, r.bos + x / p.NG, r.kvh * p.G + h, e, D, y);
 }
 
 // ------------------------------------------------------------------ host
 // Octets per pass: enough for the new tokens of an even batch (a unit's rows then read
-// the cache once), up to the four, or 512 / D, whose outputs fit the registers.
+// the cache once), up to the four whose outputs fit the registers.
 int octets_per_pass(int num_seqs, int total, int Nq, int Nkv, int D, bool bf) {
   if (!bf) return 1;
   const int64_t want = (int64_t)((total + num_seqs - 1) / num_seqs) * ((Nq / Nkv + 7) / 8);
   int nt = 1;
-  while (nt < want && nt < 4 && nt * 2 * D <= 512) nt *= 2;
+  while (nt < want && nt < 4) nt *= 2;
   return nt;
 }
 
@@ -897,7 +903,7 @@ cudaError_t launch_c(const PagedAttnArgs& a, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < 64) ready[dev] = true;
   }
-  const int grid = num_sms();
+  const int grid = std::min(num_sms(), kMaxCtas);
   Params p{};
   p.a = a;
   p.G = a.Nq / a.Nkv;
@@ -917,10 +923,8 @@ cudaError_t launch_c(const PagedAttnArgs& a, cudaStream_t s) {
   fn<<<grid, C::THREADS, C::SMEM, s>>>(mk, mv, p);
   e = cudaGetLastError();
   if (e != cudaSuccess || p.align) return e;
-  // rows spread over blocks when few units can be cut, else one block per cut unit
-  const int64_t units = (int64_t)a.Nkv * (a.num_seqs + (int64_t)a.total * p.NG / NT);
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(grid, units >= 64 ? 1 : 8);
+  cfg.gridDim = dim3(grid, C::ROWS);
   cfg.blockDim = dim3(kJoinThreads);
   cfg.stream = s;
   cudaLaunchAttribute at{};
@@ -928,17 +932,14 @@ cudaError_t launch_c(const PagedAttnArgs& a, cudaStream_t s) {
   at.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, paged_attn_join_kernel<T, D>, p, C::ROWS);
+  return cudaLaunchKernelEx(&cfg, paged_attn_join_kernel<T, D>, p);
 }
 
 template <int D>
 cudaError_t launch_bf16(const PagedAttnArgs& a, int nt, cudaStream_t s) {
   if (nt == 1) return launch_c<bf16, D, 1>(a, s);
   if (nt == 2) return launch_c<bf16, D, 2>(a, s);
-  if constexpr (D <= 128) {
-    if (nt == 4) return launch_c<bf16, D, 4>(a, s);
-  }
-  return cudaErrorInvalidValue;
+  return launch_c<bf16, D, 4>(a, s);
 }
 
 }  // namespace
@@ -946,7 +947,7 @@ cudaError_t launch_bf16(const PagedAttnArgs& a, int nt, cudaStream_t s) {
 size_t paged_attn_workspace_bytes(int num_seqs, int total, int Nq, int Nkv, int D) {
   // the same for every type and table: the caller may size it before those are known
   const int rows = octets_per_pass(num_seqs, total, Nq, Nkv, D, true) * 8;
-  const size_t grid = num_sms();
+  const size_t grid = std::min(num_sms(), kMaxCtas);
   return align16(sizeof(SplitRec) * grid) + align16(2 * grid * rows * 2 * 4) + 2 * grid * rows * D * 4;
 }
 
