@@ -8,8 +8,10 @@ RuntimeError is raised.
 """
 
 import ctypes
+import functools
 import math
 import os
+import struct
 
 import torch
 
@@ -142,7 +144,8 @@ def _tdt(code):
 
 
 def _stream():
-    return torch.cuda.current_stream().cuda_stream
+    # the handle of torch.cuda.current_stream() without its Stream object: 0.1 against 3.0 us on a Grace host
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
 
 
 def _dims(num_seqs, total, Nk, Nv, Dk, Dv):
@@ -380,12 +383,47 @@ def mixer_prefill(mixed_qkv, conv_w, a, b, A_log, dt_bias, z, norm_w, Nk, Nv, Dk
 
 
 # --- softmax attention over a paged cache ---------------------------------------------
+#
+# These calls take a few us on the GPU, so their marshalling is kept short: the C structs are
+# packed as bytes (their layouts are those of the Structures above) and passed by address.
 
-def _same_device(*tensors):
+_pack_dims = struct.Struct('@5i').pack
+_pack_heads = struct.Struct('@Pqq').pack
+_pack_norm_rope = struct.Struct('@PPfiiiPP').pack
+_pack_cache = struct.Struct('@PPqqqiiiPP').pack
+_fast = {}
+
+
+def _fn(name):
+    """The library function with its struct arguments taken as addresses of packed bytes."""
+    f = _fast.get(name)
+    if f is None:
+        f = lib()[name]                                       # a function object of its own
+        args, f.restype = _SIGS[name]
+        f.argtypes = [_P if hasattr(a, 'contents') else a for a in args]
+        _fast[name] = f
+    return f
+
+
+def _on_device(first, *tensors):
     """The library launches on the current device: every tensor has to live there."""
+    dev = first.get_device()
+    if dev < 0 or dev != torch._C._cuda_getDevice():
+        raise ValueError('expected CUDA tensors on the current device')
     for t in tensors:
-        if t is not None and (not t.is_cuda or t.device.index != torch.cuda.current_device()):
+        if t is not None and t.get_device() != dev:
             raise ValueError('expected CUDA tensors on the current device')
+
+
+def _addr(t, dtype, what):
+    """Address of an optional contiguous tensor of the given type (0: none)."""
+    if t is None:
+        return 0
+    if t.dtype != dtype:
+        raise ValueError('%s must be %s' % (what, str(dtype)[6:]))
+    if not t.is_contiguous():
+        raise ValueError('%s must be contiguous' % what)
+    return t.data_ptr()
 
 
 def _heads(t, what):
@@ -394,63 +432,65 @@ def _heads(t, what):
         return None
     if t.dim() != 3:
         raise ValueError('%s must be [tokens, heads, head_dim]' % what)
-    (T, H, D), (ts, hs, es) = t.shape, t.stride()
+    ts, hs, es = t.stride()
     if es != 1:
         raise ValueError('the head rows of %s must be contiguous' % what)
+    T, H, D = t.shape
     # a stride over an axis of one entry is never used: any value may stand there
-    return gdn_heads(t.data_ptr(), ts if T > 1 else H * D, hs if H > 1 else D)
-
-
-def _int32(t, what):
-    if t is not None and t.dtype != torch.int32:
-        raise ValueError('%s must be int32' % what)
-    return t
+    return _pack_heads(t.data_ptr(), ts if T > 1 else H * D, hs if H > 1 else D)
 
 
 def _norm_rope(q_norm_w, k_norm_w, norm_eps, cos_sin, positions, interleaved, T, D):
-    rot = 0
+    rot = maxpos = 0
     if cos_sin is not None:
         if cos_sin.dim() != 2:
             raise ValueError('cos_sin must be [positions, rotary_dim]')
-        rot = cos_sin.shape[1]
+        maxpos, rot = cos_sin.shape
+        if rot == 0:
+            maxpos = 0
     for w in (q_norm_w, k_norm_w):
         if w is not None and w.numel() != D:
             raise ValueError('a norm weight has head_dim elements')
     if positions is not None and positions.numel() != T:
         raise ValueError('positions has one entry per token')
-    return gdn_norm_rope(_ptr(_f32(q_norm_w)), _ptr(_f32(k_norm_w)), norm_eps, rot, 1 if interleaved else 0,
-                         cos_sin.shape[0] if rot else 0, _ptr(_f32(cos_sin)), _ptr(_int32(positions, 'positions')))
+    return _pack_norm_rope(_addr(q_norm_w, torch.float32, 'q_norm_w'), _addr(k_norm_w, torch.float32, 'k_norm_w'),
+                           norm_eps, rot, 1 if interleaved else 0, maxpos,
+                           _addr(cos_sin, torch.float32, 'cos_sin') if rot else 0,
+                           _addr(positions, torch.int32, 'positions'))
 
 
 def _cache(k_cache, v_cache, block_table, kv_lens, Nkv, D, num_seqs):
     """Checks the cache's tensors against the call's sizes and packs them."""
-    if k_cache.dim() != 4 or k_cache.shape != v_cache.shape or k_cache.dtype != v_cache.dtype:
+    shape = k_cache.shape
+    if len(shape) != 4 or v_cache.shape != shape or k_cache.dtype != v_cache.dtype:
         raise ValueError('k_cache and v_cache share the shape [pages, kv heads, page size, head_dim] and a dtype')
-    pages, H, P, E = k_cache.shape
+    pages, H, P, E = shape
     if H != Nkv or E != D:
         raise ValueError('the cache holds %d heads of %d, the call has %d of %d' % (H, E, Nkv, D))
-
-    def strides(t):
-        ps, hs, ss, es = t.stride()
-        if es != 1:
-            raise ValueError('the head rows of the cache must be contiguous')
-        # a stride over an axis of one entry is never used: any value may stand there
-        return (ps if pages > 1 else H * P * E, hs if H > 1 else P * E, ss if P > 1 else E)
-
-    ps, hs, ss = strides(k_cache)
-    if strides(v_cache) != (ps, hs, ss):
+    ps, hs, ss, es = stride = k_cache.stride()
+    if es != 1 or (v_cache.stride(3) != 1 and E > 1):
+        raise ValueError('the head rows of the cache must be contiguous')
+    # a stride over an axis of one entry is never used: any value may stand there
+    if pages == 1 or H == 1 or P == 1:
+        def used(st):
+            return (st[0] if pages > 1 else H * P * E, st[1] if H > 1 else P * E, st[2] if P > 1 else E)
+        ps, hs, ss = used(stride)
+        same = used(v_cache.stride()) == (ps, hs, ss)
+    else:
+        same = v_cache.stride() == stride
+    if not same:
         raise ValueError('k_cache and v_cache must have the same strides')
     if block_table.dim() != 2 or block_table.shape[0] != num_seqs or kv_lens.numel() != num_seqs:
         raise ValueError('block_table is [sequences, pages] and kv_lens [sequences]')
-    return gdn_paged_cache(k_cache.data_ptr(), v_cache.data_ptr(), ps, hs, ss, pages, P, block_table.shape[1],
-                           _ptr(_int32(block_table, 'block_table')), _ptr(_int32(kv_lens, 'kv_lens')))
+    return _pack_cache(k_cache.data_ptr(), v_cache.data_ptr(), ps, hs, ss, pages, P, block_table.shape[1],
+                       _addr(block_table, torch.int32, 'block_table'), _addr(kv_lens, torch.int32, 'kv_lens'))
 
 
 def _out(t, shape, dtype, device, what):
     if t is None:
         return torch.empty(shape, dtype=dtype, device=device)
-    if t.shape != torch.Size(shape):
-        raise ValueError('%s must have the shape %s' % (what, tuple(shape)))
+    if tuple(t.shape) != shape or not t.is_contiguous():
+        raise ValueError('%s must be contiguous and have the shape %s' % (what, shape))
     return t
 
 
@@ -459,22 +499,27 @@ def qk_norm_rope(q, k=None, cos_sin=None, q_norm_w=None, k_norm_w=None, position
     """gdn_qk_norm_rope: per-head RMSNorm and rotation of q [tokens, Nq, D] and k [tokens, Nkv, D].
     Returns (q_out, k_out); ``positions`` default to each token's index in its sequence."""
     T, Nq, D = q.shape
-    Nkv = k.shape[1] if k is not None else Nq
-    if k is not None and (k.shape != (T, Nkv, D) or k.dtype != q.dtype):
-        raise ValueError('q and k share tokens, head_dim and dtype')
-    _same_device(q, k, cos_sin, q_norm_w, k_norm_w, positions, cu_seqlens, q_out, k_out)
+    Nkv = Nq
+    if k is not None:
+        Nkv = k.shape[1]
+        if k.shape != (T, Nkv, D) or k.dtype != q.dtype:
+            raise ValueError('q and k share tokens, head_dim and dtype')
+    _on_device(q, k, cos_sin, q_norm_w, k_norm_w, positions, cu_seqlens, q_out, k_out)
+    cu = 0
     if cu_seqlens is not None:
-        num_seqs = _int32(cu_seqlens, 'cu_seqlens').numel() - 1
+        cu = _addr(cu_seqlens, torch.int32, 'cu_seqlens')
+        num_seqs = cu_seqlens.numel() - 1
     q_out = _out(q_out, (T, Nq, D), out_dtype, q.device, 'q_out')
     if k is not None:
         k_out = _out(k_out, (T, Nkv, D), q_out.dtype, q.device, 'k_out')
         if k_out.dtype != q_out.dtype:
             raise ValueError('q_out and k_out share a dtype')
-    d = gdn_attn_dims(num_seqs, T, Nq, Nkv, D)
-    nr = _norm_rope(q_norm_w, k_norm_w, norm_eps, cos_sin, positions, interleaved, T, D)
-    st = lib().gdn_qk_norm_rope(d, _ptr(cu_seqlens), _heads(q, 'q'), _heads(k, 'k'), _dt(q), nr, _ptr(q_out),
-                                _ptr(k_out) if k is not None else None, _dt(q_out), _stream())
-    _check(st, 'gdn_qk_norm_rope')
+    st = _fn('gdn_qk_norm_rope')(
+        _pack_dims(num_seqs, T, Nq, Nkv, D), cu, _heads(q, 'q'), _heads(k, 'k'), _dt(q),
+        _norm_rope(q_norm_w, k_norm_w, norm_eps, cos_sin, positions, interleaved, T, D), q_out.data_ptr(),
+        k_out.data_ptr() if k is not None else 0, _dt(q_out), _stream())
+    if st:
+        _check(st, 'gdn_qk_norm_rope')
     return q_out, k_out
 
 
@@ -492,20 +537,25 @@ def paged_kv_append(k, v, k_cache, v_cache, block_table, kv_lens, q=None, cos_si
         Nq = q.shape[1]
         if q.shape != (T, Nq, D) or q.dtype != k.dtype:
             raise ValueError('q shares tokens, head_dim and dtype with k')
-    _same_device(k, v, k_cache, v_cache, block_table, kv_lens, q, cos_sin, q_norm_w, k_norm_w, positions,
-                 cu_seqlens, q_out)
+    _on_device(k, v, k_cache, v_cache, block_table, kv_lens, q, cos_sin, q_norm_w, k_norm_w, positions,
+               cu_seqlens, q_out)
     num_seqs = kv_lens.numel()
-    if cu_seqlens is not None and _int32(cu_seqlens, 'cu_seqlens').numel() != num_seqs + 1:
-        raise ValueError('cu_seqlens has one entry more than kv_lens')
-    c = _cache(k_cache, v_cache, block_table, kv_lens, Nkv, D, num_seqs)
+    cu = 0
+    if cu_seqlens is not None:
+        cu = _addr(cu_seqlens, torch.int32, 'cu_seqlens')
+        if cu_seqlens.numel() != num_seqs + 1:
+            raise ValueError('cu_seqlens has one entry more than kv_lens')
+    cache = _cache(k_cache, v_cache, block_table, kv_lens, Nkv, D, num_seqs)
+    qo, qdt = 0, GDN_BF16
     if q is not None:
         q_out = _out(q_out, (T, Nq, D), out_dtype, q.device, 'q_out')
-    d = gdn_attn_dims(num_seqs, T, Nq, Nkv, D)
-    nr = _norm_rope(q_norm_w, k_norm_w, norm_eps, cos_sin, positions, interleaved, T, D)
-    st = lib().gdn_paged_kv_append(d, _ptr(cu_seqlens), _heads(q, 'q'), _heads(k, 'k'), _heads(v, 'v'), _dt(k), nr, c,
-                                   _dt(k_cache), _ptr(q_out) if q is not None else None,
-                                   _dt(q_out) if q is not None else GDN_BF16, _stream())
-    _check(st, 'gdn_paged_kv_append')
+        qo, qdt = q_out.data_ptr(), _dt(q_out)
+    st = _fn('gdn_paged_kv_append')(
+        _pack_dims(num_seqs, T, Nq, Nkv, D), cu, _heads(q, 'q'), _heads(k, 'k'), _heads(v, 'v'), _dt(k),
+        _norm_rope(q_norm_w, k_norm_w, norm_eps, cos_sin, positions, interleaved, T, D), cache, _dt(k_cache),
+        qo, qdt, _stream())
+    if st:
+        _check(st, 'gdn_paged_kv_append')
     return q_out if q is not None else None
 
 
@@ -516,6 +566,11 @@ def paged_attn_decode_workspace_size(num_seqs, total, Nq, Nkv, D):
     return n.value
 
 
+@functools.lru_cache(maxsize=256)
+def _attn_workspace_size(device, num_seqs, total, Nq, Nkv, D):
+    return paged_attn_decode_workspace_size(num_seqs, total, Nq, Nkv, D)
+
+
 def paged_attn_decode(q, k_cache, v_cache, block_table, kv_lens, scale=None, gate=None, cu_seqlens=None,
                       out_dtype=torch.bfloat16, o=None, workspace=None):
     """gdn_paged_attn_decode: attention of the new tokens q [tokens, Nq, D] (one or a few per sequence, bounds
@@ -523,22 +578,28 @@ def paged_attn_decode(q, k_cache, v_cache, block_table, kv_lens, scale=None, gat
     T, Nq, D = q.shape
     if k_cache.dtype != q.dtype or (gate is not None and (gate.dtype != q.dtype or gate.shape != q.shape)):
         raise ValueError('q, gate and the cache share a dtype; gate has the shape of q')
-    _same_device(q, k_cache, v_cache, block_table, kv_lens, gate, cu_seqlens, o, workspace)
+    _on_device(q, k_cache, v_cache, block_table, kv_lens, gate, cu_seqlens, o, workspace)
     num_seqs = kv_lens.numel()
-    if cu_seqlens is not None and _int32(cu_seqlens, 'cu_seqlens').numel() != num_seqs + 1:
-        raise ValueError('cu_seqlens has one entry more than kv_lens')
+    cu = 0
+    if cu_seqlens is not None:
+        cu = _addr(cu_seqlens, torch.int32, 'cu_seqlens')
+        if cu_seqlens.numel() != num_seqs + 1:
+            raise ValueError('cu_seqlens has one entry more than kv_lens')
     Nkv = k_cache.shape[1]
-    c = _cache(k_cache, v_cache, block_table, kv_lens, Nkv, D, num_seqs)
+    cache = _cache(k_cache, v_cache, block_table, kv_lens, Nkv, D, num_seqs)
     o = _out(o, (T, Nq, D), out_dtype, q.device, 'o')
-    ws_bytes = paged_attn_decode_workspace_size(num_seqs, T, Nq, Nkv, D)
-    if workspace is None and ws_bytes > 0:
-        workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=q.device)
-    d = gdn_attn_dims(num_seqs, T, Nq, Nkv, D)
-    st = lib().gdn_paged_attn_decode(d, _ptr(cu_seqlens), _heads(q, 'q'), _heads(gate, 'gate'), _dt(q), c,
-                                     1.0 / math.sqrt(D) if scale is None else scale, _ptr(o), _dt(o),
-                                     _ptr(workspace), workspace.numel() * workspace.element_size()
-                                     if workspace is not None else 0, _stream())
-    _check(st, 'gdn_paged_attn_decode')
+    if workspace is None:
+        ws_bytes = _attn_workspace_size(q.get_device(), num_seqs, T, Nq, Nkv, D)
+        if ws_bytes > 0:
+            workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=q.device)
+    else:
+        ws_bytes = workspace.numel() * workspace.element_size()
+    st = _fn('gdn_paged_attn_decode')(
+        _pack_dims(num_seqs, T, Nq, Nkv, D), cu, _heads(q, 'q'), _heads(gate, 'gate'), _dt(q), cache,
+        1.0 / math.sqrt(D) if scale is None else scale, o.data_ptr(), _dt(o),
+        0 if workspace is None else workspace.data_ptr(), ws_bytes, _stream())
+    if st:
+        _check(st, 'gdn_paged_attn_decode')
     return o
 
 

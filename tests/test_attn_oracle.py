@@ -149,6 +149,19 @@ def test_null_structs(gdn):
     assert _rope(gdn, nr=False) == gdn.GDN_ERR_INVALID_ARG
 
 
+def test_packed_structs_have_the_c_layout(gdn):
+    h = gdn.gdn_heads.from_buffer_copy(gdn._pack_heads(5, -6, 7))
+    assert (h.data, h.token_stride, h.head_stride) == (5, -6, 7)
+    vals = (1, 2, 0.5, 4, 5, 6, 7, 8)
+    n = gdn.gdn_norm_rope.from_buffer_copy(gdn._pack_norm_rope(*vals))
+    assert tuple(getattr(n, f) for f, _ in gdn.gdn_norm_rope._fields_) == vals
+    vals = tuple(range(1, 11))
+    c = gdn.gdn_paged_cache.from_buffer_copy(gdn._pack_cache(*vals))
+    assert tuple(getattr(c, f) for f, _ in gdn.gdn_paged_cache._fields_) == vals
+    d = gdn.gdn_attn_dims.from_buffer_copy(gdn._pack_dims(1, 2, 3, 4, 5))
+    assert tuple(getattr(d, f) for f, _ in gdn.gdn_attn_dims._fields_) == (1, 2, 3, 4, 5)
+
+
 def test_binding_refusals(gdn):
     bf = torch.bfloat16
     q, kc = torch.zeros(2, 8, 64, dtype=bf), torch.zeros(3, 2, 16, 64, dtype=bf)
@@ -168,7 +181,9 @@ def test_binding_refusals(gdn):
     with pytest.raises(ValueError, match='block_table'):
         gdn._cache(kc, kc, bt, lens[:1], 2, 64, 2)
     with pytest.raises(ValueError, match='int32'):
-        gdn._int32(lens.long(), 'kv_lens')
+        gdn._cache(kc, kc, bt, lens.long(), 2, 64, 2)
+    with pytest.raises(ValueError, match='contiguous'):
+        gdn._cache(kc, kc, torch.zeros(1, 2, dtype=torch.int32).T.expand(2, 2), lens, 2, 64, 2)
     with pytest.raises(ValueError, match='contiguous'):
         gdn._heads(torch.zeros(2, 64, 8).transpose(1, 2), 'q')
     with pytest.raises(ValueError, match='norm weight'):
