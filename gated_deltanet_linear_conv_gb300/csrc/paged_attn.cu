@@ -9,23 +9,25 @@
 //
 // Rows.  The 8 columns of a product tile (an octet) are query heads of one token and one
 // kv head; all its columns see the same cache indices.  A unit is (sequence, kv head, NT
-// consecutive octets); its cache indices split into tiles of 16 KB of K and 16 KB of V.
+// consecutive octets); its cache indices split into tiles of 8 KB of K and 8 KB of V.
 //
 // Work split.  All tiles of all units, laid end to end, are cut into one equal range per
-// CTA (one CTA per SM), from kv_lens as they stand on the device: ragged batches and a
-// single long context keep every SM equally busy, and neither the host nor a captured
-// graph needs the lengths.  A unit inside one range is finished by its CTA; the pieces of
-// a unit that crosses ranges (at most one cut per CTA) go to the workspace, unnormalised
-// with their maxima and sums, and a second small kernel joins them in order.  With short
-// tables (no unit can exceed kAlignTiles tiles) ranges end at unit borders instead and no
-// second kernel runs.
+// CTA (two CTAs per SM, one's starts and joins under the other's stream), from kv_lens as
+// they stand on the device: ragged batches and a single long context keep every SM equally
+// busy, and neither the host nor a captured graph needs the lengths.  A unit inside one
+// range is finished by its CTA; the pieces of a unit that crosses ranges (at most one cut
+// per CTA) go to the workspace, unnormalised with their maxima and sums, and a second small
+// kernel joins them in order.  With short tables (no unit can exceed kAlignTiles tiles)
+// ranges end at unit borders instead and no second kernel runs.
 //
 // Inside a CTA a producer warp walks the range: it looks the page ids up and issues TMA
 // boxes of gcd(page size, tile) slots (so any page size tiles exactly; slots past the end
 // of a sequence come as the out-of-range zero fill) into a ring of stages, and the query
-// rows of each unit by bulk copies.  Consumer warps each take 16-token (bf16) or 4-token
+// rows of each unit by bulk copies.  Four consumer warps take 16-token (bf16) or 4-token
 // (float32) slices with a maximum, sum and output of their own, joined through shared
-// memory once per unit.
+// memory once per unit.  With many rows (NT * D > 256) DS of them share a slice: each
+// computes the weights of NT / DS octets, they exchange them, and each accumulates D / DS
+// columns of the output of all octets, so that a warp never holds more than 64 accumulators.
 
 #include <numeric>
 
@@ -37,10 +39,11 @@
 namespace gdn {
 namespace {
 
-constexpr int kStageHalf = 16384;                  // bytes of K (and of V) in a stage
-constexpr int kAlignTiles = 8;                     // no unit longer than this: ranges end at unit borders
-constexpr int kMinTiles = 2;                       // tiles of a range at least (fewer CTAs for little work)
-constexpr int kMaxCtas = 256;                      // CTAs, and so pieces of a unit, at most
+constexpr int kStageHalf = 8192;                   // bytes of K (and of V) in a stage
+constexpr int kAlignTiles = 16;                    // no unit longer than this: ranges end at unit borders
+constexpr int kMinTiles = 4;                       // tiles of a range at least (fewer CTAs for little work)
+constexpr int kOcc = 2;                            // CTAs per SM
+constexpr int kMaxCtas = 512;                      // CTAs, and so pieces of a unit, at most
 constexpr uint64_t kWaitNs = 2000000000ull;        // bound of every wait
 constexpr uint32_t kPollCap = 1u << 28;
 constexpr float kLog2e = 1.4426950408889634f;
@@ -51,10 +54,10 @@ struct Cfg {
   static constexpr bool BF = sizeof(T) == 2;
   static constexpr int NT = NT_;                                   // octets per pass
   static constexpr int ROWS = NT * 8;
-  static constexpr int CW = 8;                                     // consumer warps
-  static constexpr int DS = BF && D == 256 ? 2 : 1;                // warps that share a slice, each with D / DS of its output
-  static constexpr int TG = CW / DS;                               // slices in work at a time
+  static constexpr int CW = 4;                                     // consumer warps
   static constexpr int THREADS = (CW + 1) * 32;
+  static constexpr int DS = BF && NT * D > 256 ? NT * D / 256 : 1; // warps that share a slice
+  static constexpr int TG = CW / DS;                               // slices in work at a time
   static constexpr int TILE = kStageHalf / (D * (int)sizeof(T));   // tokens per stage
   static constexpr int SLICE = BF ? 16 : 4;                        // tokens per warp step
   static constexpr int SL = TILE / SLICE;                          // slices per stage
@@ -62,18 +65,20 @@ struct Cfg {
   static constexpr int QPITCH = D * (int)sizeof(T) + 16;           // bytes; padded: ldmatrix without conflicts
   static constexpr int QBYTES = ROWS * QPITCH;
   static constexpr int JP = D + 4;                                 // join row pitch (floats)
-  static constexpr int JOIN = TG * 8 * JP * 4 + TG * 8 * 2 * 4;
+  static constexpr int JOIN = TG * ROWS * (JP + 2) * 4;
+  static constexpr int XW = NT * 32 * 16, XA = NT * 8 * 4;         // weights and factors of a shared slice
+  static constexpr int XBYTES = DS > 1 ? TG * 2 * (XW + XA) : 0;
   static constexpr int HEAD = 1024;
-  static constexpr int FIXED = HEAD + 2 * QBYTES + JOIN;
-  static constexpr int MOST = 227 * 1024 - 1024;                   // 1024: alignment of the ring
-  // Where a stage has fewer slices than there are warps, GROUPS sets of warps take the stages
+  static constexpr int FIXED = HEAD + QBYTES + JOIN + XBYTES;
+  static constexpr int MOST = 113 * 1024 - 1024;                   // two CTAs per SM; 1024: alignment of the ring
+  // Where a stage has fewer slices than are in work, GROUPS sets of warps take the stages
   // in turn; the ring is a multiple of them, so that a stage always has the same readers (a
   // warp two rounds ahead of another's would take a phase that is still to come for done).
   static constexpr int GROUPS = TG / USERS;
   static constexpr int FIT = (MOST - FIXED) / (2 * kStageHalf) < 6 ? (MOST - FIXED) / (2 * kStageHalf) : 6;
   static constexpr int STAGES = FIT - FIT % GROUPS;
   static constexpr int SMEM = FIXED + STAGES * 2 * kStageHalf + 1024;
-  static_assert(STAGES >= 3 && TG % USERS == 0 && STAGES % GROUPS == 0, "ring");
+  static_assert(SL >= 1 && STAGES >= 3 && TG % USERS == 0 && STAGES % GROUPS == 0, "ring");
 };
 
 // One piece of a unit, from the producer to the consumers (and, unjoined, to the join kernel).
@@ -85,10 +90,30 @@ struct Piece {
 };
 // A unit that starts in a CTA's range and ends behind it; CTA c's is record c.
 struct SplitRec {
-  int valid, bos, x0, nvalid, kvh, geff;
-  int64_t end, total;      // the unit's end in the laid-out tiles; all tiles
+  int valid, bos, x0, nvalid, kvh;
+  int pieces;              // CTAs c .. c + pieces - 1 hold its pieces
 };
-static_assert(sizeof(SplitRec) == 40, "");
+
+// Bounds of the ranges: CTA c of n takes [at(c), at(c + 1)) of `total` tiles.
+struct Ranges {
+  int64_t q;
+  int r, n;
+  __device__ __forceinline__ Ranges(int64_t total, int ctas) : n(ctas) {
+    if (total >> 31) {
+      q = total / ctas;
+      r = (int)(total % ctas);
+    } else {
+      q = (uint32_t)total / (uint32_t)ctas;
+      r = (int)((uint32_t)total - (uint32_t)q * (uint32_t)ctas);
+    }
+  }
+  __device__ __forceinline__ int64_t at(int c) const { return q * c + min(c, r); }
+  // CTAs that start before position `end` > 0
+  __device__ __forceinline__ int before(int64_t end) const {
+    const int64_t wide = (q + 1) * r;
+    return end <= wide ? (int)((end + q) / (q + 1)) : r + (int)((end - wide + q - 1) / q);
+  }
+};
 
 __host__ __device__ constexpr size_t align16(size_t x) { return (x + 15) & ~(size_t)15; }
 
@@ -170,11 +195,20 @@ __device__ __forceinline__ Seq load_seq(const PagedAttnArgs& a, int s, int* err 
   if (!ok && err != nullptr) raise_error(err, kDevErrSeqlens);
   return {bos, n, n > 0 ? len : 0};
 }
+// x / d for 0 <= x / d < 2^31, by the short division where x allows it.
+__device__ __forceinline__ int div_small(int64_t x, int d) {
+  return x >> 32 ? (int)(x / d) : (int)((uint32_t)x / (uint32_t)d);
+}
 template <typename C>
 __device__ __forceinline__ int seq_tiles(const Seq& q) { return (q.len + C::TILE - 1) / C::TILE; }
 template <typename C>
 __device__ __forceinline__ int seq_groups(const Params& p, const Seq& q) {   // octet groups per kv head
   return (int)(((int64_t)q.n * p.NG + C::NT - 1) / C::NT);
+}
+
+template <typename C>
+__device__ __forceinline__ int64_t seq_work(const Params& p, const Seq& q) {
+  return q.len == 0 ? 0 : (int64_t)seq_tiles<C>(q) * seq_groups<C>(p, q) * p.a.Nkv;
 }
 
 // y = o * sigmoid(gate), four elements of (token t, head h) from d.
@@ -205,49 +239,51 @@ struct TcWarp {
   using C = Cfg<bf16, D, NT>;
   static constexpr int KS = D / 16;
   static constexpr int OS = KS / C::DS;            // 16-row blocks of O^T that this warp holds
-  static constexpr bool QREG = NT * D <= 256;      // query fragments stay in registers
-  static constexpr int CH = NT <= 2 ? 2 : 1;       // score accumulators: shorter chains of dependent products
+  static constexpr int NO = NT / C::DS;            // octets whose weights it computes
+  static_assert(OS * NT <= 16 && NO >= 1, "64 accumulators");
   float o[NT][OS][4];
-  float m[NT][2], l[NT][2];
-  uint32_t qf[QREG ? NT : 1][QREG ? KS : 1][2];
-  uint32_t qaddr;
-  int d0;                                          // first of this warp's blocks
+  float m[NO][2], l[NO][2];
+  uint32_t qf[NO][KS][2];
+  int d0, n0;                                      // first of its blocks and octets
+  uint32_t xw;                                     // exchange buffer of the warps that share its slices
+  uint32_t flip;
 
-  __device__ __forceinline__ void start(const uint8_t* q, int share, int lane) {
+  __device__ __forceinline__ void start(const uint8_t* q, int share, uint8_t* x, int lane) {
     d0 = share * OS;
+    n0 = share * NO;
+    xw = tc::smem_u32(x);
+    flip = 0;
     // x4: two k steps of one octet; lanes 8i..8i+7 give the rows of matrix i
-    qaddr = tc::smem_u32(q) + (lane & 7) * C::QPITCH + (lane >> 3) * 16;
-    if (QREG) {
+    const uint32_t qaddr = tc::smem_u32(q) + (n0 * 8 + (lane & 7)) * C::QPITCH + (lane >> 3) * 16;
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+    for (int k = 0; k < NO; ++k) {
 #pragma unroll
-        for (int ks = 0; ks < KS; ks += 2) {
-          uint32_t r[4];
-          ldsm4(qaddr + nt * 8 * C::QPITCH + ks * 32, r);
-          qf[nt][ks][0] = r[0]; qf[nt][ks][1] = r[1];
-          qf[nt][ks + 1][0] = r[2]; qf[nt][ks + 1][1] = r[3];
-        }
+      for (int ks = 0; ks < KS; ks += 2) {
+        uint32_t r[4];
+        ldsm4(qaddr + k * 8 * C::QPITCH + ks * 32, r);
+        qf[k][ks][0] = r[0]; qf[k][ks][1] = r[1];
+        qf[k][ks + 1][0] = r[2]; qf[k][ks + 1][1] = r[3];
+      }
+      m[k][0] = m[k][1] = -INFINITY;
+      l[k][0] = l[k][1] = 0.f;
     }
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      m[nt][0] = m[nt][1] = -INFINITY;
-      l[nt][0] = l[nt][1] = 0.f;
+    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int i = 0; i < OS; ++i)
 #pragma unroll
         for (int e = 0; e < 4; ++e) o[nt][i][e] = 0.f;
-    }
   }
 
   // Slice of the 16 tokens from tok0, rows j0.. of the stage; lim(nt): tokens octet nt sees.
   template <typename Lim>
   __device__ __forceinline__ void slice(uint8_t* ks_, uint8_t* vs_, int j0, int tok0, int nvalid, float c, Lim lim,
-                                        int lane) {
-    float s[NT][4], s1[NT][4];
+                                        int tw, int lane) {
+    float s[NO][4], s1[NO][4];                     // two accumulators: half the chain of dependent products
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+    for (int k = 0; k < NO; ++k)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) s[nt][e] = s1[nt][e] = 0.f;
+      for (int e = 0; e < 4; ++e) s[k][e] = s1[k][e] = 0.f;
     {
       const int row = j0 + (lane & 15);
       const uint32_t base = tc::smem_u32(ks_) + row * 128;
@@ -259,64 +295,80 @@ struct TcWarp {
         ldsm4(blk + (((uint32_t)((ks & 3) * 2 + (lane >> 4)) ^ sw) << 4), a0);
         ldsm4(blk + (((uint32_t)((ks & 3) * 2 + 2 + (lane >> 4)) ^ sw) << 4), a1);
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          if (QREG) {
-            mma16816(s[nt], a0, qf[nt][ks][0], qf[nt][ks][1]);
-            mma16816(CH == 2 ? s1[nt] : s[nt], a1, qf[nt][ks + 1][0], qf[nt][ks + 1][1]);
-          } else {
-            uint32_t r[4];
-            ldsm4(qaddr + nt * 8 * C::QPITCH + ks * 32, r);
-            mma16816(s[nt], a0, r[0], r[1]);
-            mma16816(CH == 2 ? s1[nt] : s[nt], a1, r[2], r[3]);
-          }
+        for (int k = 0; k < NO; ++k) {
+          mma16816(s[k], a0, qf[k][ks][0], qf[k][ks][1]);
+          mma16816(s1[k], a1, qf[k][ks + 1][0], qf[k][ks + 1][1]);
         }
       }
     }
     const bool tail = tok0 + 16 > lim(0);          // octets come in order of their token: lim(0) is the least
-    const int g = lane >> 2;
-    uint32_t hi[NT][2], lo[NT][2];
+    const int g = lane >> 2, t = lane & 3;
+    uint32_t w[NT][4];                             // weights: high parts of both 8-token halves, low parts
+    float al[NT][2];                               // factors of the outputs so far
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
+    for (int k = 0; k < NO; ++k) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) s[nt][e] = (CH == 2 ? s[nt][e] + s1[nt][e] : s[nt][e]) * c;
+      for (int e = 0; e < 4; ++e) s[k][e] = (s[k][e] + s1[k][e]) * c;
       if (tail) {
-        const int last = lim(nt) - tok0;
-        if (g >= last) s[nt][0] = s[nt][1] = -INFINITY;
-        if (g + 8 >= last) s[nt][2] = s[nt][3] = -INFINITY;
+        const int last = lim(n0 + k) - tok0;
+        if (g >= last) s[k][0] = s[k][1] = -INFINITY;
+        if (g + 8 >= last) s[k][2] = s[k][3] = -INFINITY;
       }
-      float mx[2] = {fmaxf(s[nt][0], s[nt][2]), fmaxf(s[nt][1], s[nt][3])};
+      float mx[2] = {fmaxf(s[k][0], s[k][2]), fmaxf(s[k][1], s[k][3])};
 #pragma unroll
       for (int off = 4; off < 32; off <<= 1) {
         mx[0] = fmaxf(mx[0], __shfl_xor_sync(0xffffffffu, mx[0], off));
         mx[1] = fmaxf(mx[1], __shfl_xor_sync(0xffffffffu, mx[1], off));
       }
-      const bool up = mx[0] > m[nt][0] || mx[1] > m[nt][1];
-      if (__any_sync(0xffffffffu, up)) {
-        float al[2];
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const float mn = fmaxf(m[nt][e], mx[e]);
-          al[e] = mn == m[nt][e] ? 1.f : exp2f(m[nt][e] - mn);     // (-inf stays -inf: no change)
-          m[nt][e] = mn;
-          l[nt][e] *= al[e];
-        }
-#pragma unroll
-        for (int i = 0; i < OS; ++i)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) o[nt][i][e] *= al[e & 1];
+      for (int e = 0; e < 2; ++e) {
+        const float mn = fmaxf(m[k][e], mx[e]);
+        al[k][e] = mn == m[k][e] ? 1.f : exp2f(m[k][e] - mn);      // (-inf stays -inf: no change)
+        m[k][e] = mn;
       }
-      const float b0 = m[nt][0] == -INFINITY ? 0.f : m[nt][0], b1 = m[nt][1] == -INFINITY ? 0.f : m[nt][1];
-      const float p0 = exp2f(s[nt][0] - b0), p1 = exp2f(s[nt][1] - b1);
-      const float p2 = exp2f(s[nt][2] - b0), p3 = exp2f(s[nt][3] - b1);
-      l[nt][0] += p0 + p2;
-      l[nt][1] += p1 + p3;
+      const float b0 = m[k][0] == -INFINITY ? 0.f : m[k][0], b1 = m[k][1] == -INFINITY ? 0.f : m[k][1];
+      const float p0 = exp2f(s[k][0] - b0), p1 = exp2f(s[k][1] - b1);
+      const float p2 = exp2f(s[k][2] - b0), p3 = exp2f(s[k][3] - b1);
+      l[k][0] = fmaf(l[k][0], al[k][0], p0 + p2);
+      l[k][1] = fmaf(l[k][1], al[k][1], p1 + p3);
       const uint32_t h0 = pack_bf16(p0, p1), h1 = pack_bf16(p2, p3);
       const float2 f0 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&h0));
       const float2 f1 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&h1));
-      hi[nt][0] = movm(h0);
-      hi[nt][1] = movm(h1);
-      lo[nt][0] = movm(pack_bf16(p0 - f0.x, p1 - f0.y));
-      lo[nt][1] = movm(pack_bf16(p2 - f1.x, p3 - f1.y));
+      w[k][0] = movm(h0);
+      w[k][1] = movm(h1);
+      w[k][2] = movm(pack_bf16(p0 - f0.x, p1 - f0.y));
+      w[k][3] = movm(pack_bf16(p2 - f1.x, p3 - f1.y));
+    }
+    if (C::DS > 1) {
+      // all octets' weights and factors through the exchange buffer; two of them in turn: a
+      // warp writes one again only after a barrier that the others reach behind their reads
+      const uint32_t xb = xw + flip * (C::XW + C::XA);
+      flip ^= 1;
+#pragma unroll
+      for (int k = 0; k < NO; ++k) {
+        asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(xb + ((n0 + k) * 32 + lane) * 16), "r"(w[k][0]),
+                     "r"(w[k][1]), "r"(w[k][2]), "r"(w[k][3]) : "memory");
+        if (g == 0)
+          asm volatile("st.shared.v2.f32 [%0], {%1,%2};" ::"r"(xb + C::XW + ((n0 + k) * 8 + 2 * t) * 4), "f"(al[k][0]),
+                       "f"(al[k][1]) : "memory");
+      }
+      tc::named_sync(2 + tw, C::DS * 32);
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(w[nt][0]), "=r"(w[nt][1]), "=r"(w[nt][2]), "=r"(w[nt][3])
+                     : "r"(xb + (nt * 32 + lane) * 16) : "memory");
+        asm volatile("ld.shared.v2.f32 {%0,%1}, [%2];" : "=f"(al[nt][0]), "=f"(al[nt][1])
+                     : "r"(xb + C::XW + (nt * 8 + 2 * t) * 4) : "memory");
+      }
+    }
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      if (__any_sync(0xffffffffu, al[nt][0] != 1.f || al[nt][1] != 1.f)) {
+#pragma unroll
+        for (int i = 0; i < OS; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[nt][i][e] *= al[nt][e & 1];
+      }
     }
     const int vrow = j0 + (lane & 7) + ((lane >> 4) << 3);
     const uint32_t vbase = tc::smem_u32(vs_) + vrow * 128;
@@ -326,60 +378,68 @@ struct TcWarp {
       const uint32_t ch = (uint32_t)((i & 3) * 2 + ((lane >> 3) & 1));
       ldsm4t(vbase + (i >> 2) * (C::TILE * 128) + ((ch ^ vsw) << 4), a);
     };
-    if (!tail) {
+    // Rows that an octet does not see may hold anything, and 0 * NaN is NaN: at the end of the
+    // visible range they are cleared in the stage, in the columns that this warp reads.
+    auto clear = [&](int last) {
+      for (int e = lane; e < (16 - last) * (2 * OS); e += 32) {
+        const int r = j0 + last + e / (2 * OS), ch = 2 * d0 + e % (2 * OS);
+        *reinterpret_cast<uint4*>(vs_ + (ch >> 3) * (C::TILE * 128) + r * 128 + ((ch & 7) << 4)) = make_uint4(0, 0, 0, 0);
+      }
+      __syncwarp();
+    };
+    if (NT > 1 && tail) {
+      // from the octet that sees most to the one that sees least
+#pragma unroll
+      for (int nt = NT - 1; nt >= 0; --nt) {
+        if (nt >= nvalid) continue;
+        clear(max(0, min(16, lim(nt) - tok0)));
+#pragma unroll
+        for (int i = 0; i < OS; ++i) {
+          uint32_t a[4];
+          vfrag(i, a);
+          mma16816(o[nt][i], a, w[nt][0], w[nt][1]);
+          mma16816(o[nt][i], a, w[nt][2], w[nt][3]);
+        }
+        __syncwarp();
+      }
+    } else {
+      if (tail) clear(min(16, lim(0) - tok0));
 #pragma unroll
       for (int i = 0; i < OS; ++i) {
         uint32_t a[4];
         vfrag(i, a);
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          mma16816(o[nt][i], a, hi[nt][0], hi[nt][1]);
-          mma16816(o[nt][i], a, lo[nt][0], lo[nt][1]);
-        }
-      }
-    } else {
-      // The end of the visible range: rows that an octet does not see may hold anything, and
-      // 0 * NaN is NaN.  They are cleared in the stage, from the octet that sees most to the
-      // one that sees least; a warp clears the columns that it reads.
+        for (int nt = 0; nt < NT; ++nt) mma16816(o[nt][i], a, w[nt][0], w[nt][1]);
 #pragma unroll
-      for (int nt = NT - 1; nt >= 0; --nt) {
-        if (nt >= nvalid) continue;
-        const int last = max(0, min(16, lim(nt) - tok0));
-        for (int e = lane; e < (16 - last) * (2 * OS); e += 32) {
-          const int r = j0 + last + e / (2 * OS), ch = 2 * d0 + e % (2 * OS);
-          *reinterpret_cast<uint4*>(vs_ + (ch >> 3) * (C::TILE * 128) + r * 128 + ((ch & 7) << 4)) = make_uint4(0, 0, 0, 0);
-        }
-        __syncwarp();
-#pragma unroll
-        for (int i = 0; i < OS; ++i) {
-          uint32_t a[4];
-          vfrag(i, a);
-          mma16816(o[nt][i], a, hi[nt][0], hi[nt][1]);
-          mma16816(o[nt][i], a, lo[nt][0], lo[nt][1]);
-        }
-        __syncwarp();
+        for (int nt = 0; nt < NT; ++nt) mma16816(o[nt][i], a, w[nt][2], w[nt][3]);
       }
-      tc::fence_proxy_async_smem();                // before the ring's next copy into these rows
     }
+    if (tail) tc::fence_proxy_async_smem();        // before the ring's next copy into the cleared rows
   }
 
-  // This warp's share of octet nt into the join buffers.
-  __device__ __forceinline__ void give(int nt, float* jo, float* jm, float* jl, int lane) {
+  // This warp's share into the join buffers (any: it took a slice).
+  __device__ __forceinline__ void give(float* jo, float* jm, float* jl, bool any, int lane) {
     const int g = lane >> 2, t = lane & 3;
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      float v = l[nt][e];
+    for (int k = 0; k < NO; ++k)
 #pragma unroll
-      for (int off = 4; off < 32; off <<= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
-      if (g == 0 && d0 == 0) {
-        jm[2 * t + e] = m[nt][e];
-        jl[2 * t + e] = v;
+      for (int e = 0; e < 2; ++e) {
+        float v = l[k][e];
+#pragma unroll
+        for (int off = 4; off < 32; off <<= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+        if (g == 0) {
+          jm[(n0 + k) * 8 + 2 * t + e] = m[k][e];
+          jl[(n0 + k) * 8 + 2 * t + e] = v;
+        }
       }
-    }
+    if (!any) return;
 #pragma unroll
-    for (int i = 0; i < OS; ++i)
+    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) jo[(2 * t + (e & 1)) * C::JP + (d0 + i) * 16 + g + (e >> 1) * 8] = o[nt][i][e];
+      for (int i = 0; i < OS; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          jo[(nt * 8 + 2 * t + (e & 1)) * C::JP + (d0 + i) * 16 + g + (e >> 1) * 8] = o[nt][i][e];
   }
 };
 
@@ -409,7 +469,7 @@ struct SimtWarp {
       x[0] = f.x; x[1] = f.y;
     }
   }
-  __device__ __forceinline__ void start(const uint8_t* qs, int, int lane) {
+  __device__ __forceinline__ void start(const uint8_t* qs, int, uint8_t*, int lane) {
 #pragma unroll
     for (int h = 0; h < 8; ++h) {
       row(qs + h * C::QPITCH, 0, lane, q[h]);
@@ -420,7 +480,8 @@ struct SimtWarp {
     l = 0.f;
   }
   template <typename Lim>
-  __device__ __forceinline__ void slice(uint8_t* ks_, uint8_t* vs_, int j0, int tok0, int, float c, Lim lim, int lane) {
+  __device__ __forceinline__ void slice(uint8_t* ks_, uint8_t* vs_, int j0, int tok0, int, float c, Lim lim, int,
+                                        int lane) {
     const int last = lim(0) - tok0;                // tokens of the slice that are visible (> 0)
     float s = 0.f;
 #pragma unroll
@@ -477,7 +538,7 @@ struct SimtWarp {
       }
     }
   }
-  __device__ __forceinline__ void give(int, float* jo, float* jm, float* jl, int lane) {
+  __device__ __forceinline__ void give(float* jo, float* jm, float* jl, bool any, int lane) {
     float v = l;
     v += __shfl_xor_sync(0xffffffffu, v, 1);
     v += __shfl_xor_sync(0xffffffffu, v, 2);
@@ -485,6 +546,7 @@ struct SimtWarp {
       jm[lane >> 2] = m;
       jl[lane >> 2] = v;
     }
+    if (!any) return;
 #pragma unroll
     for (int h = 0; h < 8; ++h)
 #pragma unroll
@@ -496,7 +558,7 @@ template <int D, int NT> struct WarpOf<float, D, NT> { using type = SimtWarp<D>;
 
 // ------------------------------------------------------------------ the main kernel
 template <typename T, int D, int NT>
-__global__ void __launch_bounds__(Cfg<T, D, NT>::THREADS, 1)
+__global__ void __launch_bounds__(Cfg<T, D, NT>::THREADS, kOcc)
 paged_attn_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
                   const __grid_constant__ Params p) {
   using C = Cfg<T, D, NT>;
@@ -505,30 +567,31 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
   extern __shared__ __align__(16) uint8_t raw[];
   uint8_t* ring = tc::smem_aligned<1024>(raw);
   uint8_t* qs = ring + C::STAGES * 2 * kStageHalf;
-  float* jo = reinterpret_cast<float*>(qs + 2 * C::QBYTES);
-  float* jm = jo + C::TG * 8 * C::JP;
-  float* jl = jm + C::TG * 8;
-  uint8_t* head = reinterpret_cast<uint8_t*>(jl + C::TG * 8);
+  uint8_t* xs = qs + C::QBYTES;
+  float* jo = reinterpret_cast<float*>(xs + C::XBYTES);
+  float* jm = jo + C::TG * C::ROWS * C::JP;
+  float* jl = jm + C::TG * C::ROWS;
+  uint8_t* head = reinterpret_cast<uint8_t*>(jl + C::TG * C::ROWS);
   uint64_t* full = reinterpret_cast<uint64_t*>(head);
   uint64_t* empty = full + C::STAGES;
   uint64_t* qfull = empty + C::STAGES;
-  uint64_t* qempty = qfull + 2;
-  Piece* piece = reinterpret_cast<Piece*>(head + 256);             // [2]
-  int64_t* scan = reinterpret_cast<int64_t*>(head + 512);          // [CW + 1] warp sums, then the start
+  uint64_t* qempty = qfull + 1;
+  Piece* piece = reinterpret_cast<Piece*>(head + 256);
+  int64_t* scan = reinterpret_cast<int64_t*>(head + 512);          // [CW + 1] warp sums
+  int64_t* from = scan + C::CW + 1;                                // where the range starts: the sequence's first tile
+  int* from_seq = reinterpret_cast<int*>(from + 1);                // and the sequence: index, bos, n, len
   volatile int* abort = reinterpret_cast<int*>(head + 768);
   const PagedAttnArgs& a = p.a;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  if (tid == 0) {
+  if (tid == C::CW * 32) {
     for (int i = 0; i < C::STAGES; ++i) {
       tc::mbar_init(full + i, 1);
       tc::mbar_init(empty + i, C::USERS * C::DS);
     }
-    for (int i = 0; i < 2; ++i) {
-      tc::mbar_init(qfull + i, 1);
-      tc::mbar_init(qempty + i, C::CW);
-    }
+    tc::mbar_init(qfull, 1);
+    tc::mbar_init(qempty, C::CW);
     *abort = 0;
     tc::fence_barrier_init();
     tc::prefetch_tmap(&mk);
@@ -538,10 +601,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
   const int per = (a.num_seqs + C::THREADS - 1) / C::THREADS;
   const int s_lo = min(a.num_seqs, tid * per), s_hi = min(a.num_seqs, s_lo + per);
   int64_t sum = 0;
-  for (int s = s_lo; s < s_hi; ++s) {
-    const Seq q = load_seq(a, s);
-    sum += (int64_t)seq_tiles<C>(q) * seq_groups<C>(p, q) * a.Nkv;
-  }
+  for (int s = s_lo; s < s_hi; ++s) sum += seq_work<C>(p, load_seq(a, s));
   int64_t inc = sum;
 #pragma unroll
   for (int off = 1; off < 32; off <<= 1) {
@@ -551,23 +611,26 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
   if (lane == 31) scan[warp] = inc;
   __syncthreads();
   int64_t before = inc - sum, total = 0;
+#pragma unroll
   for (int w = 0; w <= C::CW; ++w) {
     if (w < warp) before += scan[w];
     total += scan[w];
   }
-  const int64_t geff = max((int64_t)1, min((int64_t)gridDim.x, total / kMinTiles));
-  const bool mine = (int64_t)blockIdx.x < geff;
-  const int64_t lo = mine ? total * blockIdx.x / geff : total;
-  const int64_t hi = mine ? total * (blockIdx.x + 1) / geff : total;
-  __syncthreads();
+  const Ranges rg(total, (int)max((int64_t)1, min((int64_t)gridDim.x, total / kMinTiles)));
+  const bool mine = (int)blockIdx.x < rg.n;
+  const int64_t lo = mine ? rg.at(blockIdx.x) : total;
+  const int64_t hi = mine ? rg.at(blockIdx.x + 1) : total;
   if (before <= lo && lo < before + sum) {
     int64_t at = before;
     for (int s = s_lo; s < s_hi; ++s) {
       const Seq q = load_seq(a, s);
-      const int64_t w = (int64_t)seq_tiles<C>(q) * seq_groups<C>(p, q) * a.Nkv;
+      const int64_t w = seq_work<C>(p, q);
       if (lo < at + w) {
-        scan[0] = s;
-        scan[1] = at;
+        *from = at;
+        from_seq[0] = s;
+        from_seq[1] = q.bos;
+        from_seq[2] = q.n;
+        from_seq[3] = q.len;
         break;
       }
       at += w;
@@ -577,119 +640,117 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
 
   if (warp == C::CW) {
     // ------------------------------------------------------------ producer
-    int s = lo < hi ? (int)scan[0] : a.num_seqs;
-    int64_t seq_at = lo < hi ? scan[1] : 0, pos = lo;
     SplitRec rec{};
     int it = 0, npiece = 0;
     bool ok = true;
-    Seq q{0, 0, 0};
-    int tiles = 0, groups = 0;
-    if (s < a.num_seqs) {
-      q = load_seq(a, s);
-      tiles = seq_tiles<C>(q);
-      groups = seq_groups<C>(p, q);
-      if (p.align) pos = seq_at + (pos - seq_at + tiles - 1) / tiles * tiles;   // the first unit that starts here
-    }
-    while (ok && pos < hi) {
-      if (pos >= seq_at + (int64_t)tiles * groups * a.Nkv) {
-        // the next sequence with work: the warp looks at 32 of them at a time
-        seq_at += (int64_t)tiles * groups * a.Nkv;
-        int base = s + 1;
-        for (;;) {
-          Seq c{0, 0, 0};
-          if (base + lane < a.num_seqs) c = load_seq(a, base + lane);
-          const uint32_t has = __ballot_sync(0xffffffffu, c.len > 0);
-          if (has != 0) {
-            const int w = __ffs(has) - 1;
-            s = base + w;
-            q.bos = __shfl_sync(0xffffffffu, c.bos, w);
-            q.n = __shfl_sync(0xffffffffu, c.n, w);
-            q.len = __shfl_sync(0xffffffffu, c.len, w);
-            break;
-          }
-          base += 32;
-          if (base >= a.num_seqs) break;           // (cannot be: pos < hi <= total)
-        }
-        if (base >= a.num_seqs) break;
-        tiles = seq_tiles<C>(q);
-        groups = seq_groups<C>(p, q);
-        continue;
-      }
-      const int unit = (int)((pos - seq_at) / tiles);
-      const int t0 = (int)((pos - seq_at) % tiles);
-      const int t1 = p.align ? tiles : (int)min((int64_t)tiles, t0 + (hi - pos));
-      const int kvh = unit / groups, x0 = (unit % groups) * NT;
-      const int nvalid = min(NT, q.n * p.NG - x0);
-      const int qslot = npiece & 1;
-      ok = wait_bar(qempty + qslot, ((npiece >> 1) & 1) ^ 1, abort);
-      if (!ok) break;
-      if (lane == 0) {
-        Piece d;
-        d.tile0 = t0; d.tile1 = t1;
-        d.slot = t0 == 0 && t1 == tiles ? -1 : 2 * (int)blockIdx.x + (t0 == 0 ? 1 : 0);
-        d.len = q.len; d.n = q.n; d.bos = q.bos; d.x0 = x0; d.nvalid = nvalid; d.kvh = kvh;
-        piece[qslot] = d;
-        if (t0 == 0 && t1 < tiles)
-          rec = {1, q.bos, x0, nvalid, kvh, (int)geff, pos + tiles, total};
-      }
-      // query rows: octet x of the sequence is token x / NG, heads (x % NG) * 8 .. of the kv head's G
-      int rows = 0;
-      for (int x = x0; x < x0 + nvalid; ++x) rows += min(8, p.G - (x % p.NG) * 8);
-      if (lane == 0) tc::mbar_arrive_expect_tx(qfull + qslot, (uint32_t)(rows * D * sizeof(T)));
-      __syncwarp();
-      for (int r = lane; r < nvalid * 8; r += 32) {
-        const int x = x0 + r / 8, oct = x % p.NG, h = oct * 8 + r % 8;
-        if (h < p.G)
-          tc::bulk_load(qs + qslot * C::QBYTES + r * C::QPITCH,
-                        static_cast<const T*>(a.q.p) + (q.bos + x / p.NG) * a.q.ts + (kvh * p.G + h) * a.q.hs,
-                        D * sizeof(T), qfull + qslot);
-      }
-      ++npiece;
-      const int32_t* bt = a.c.bt + (int64_t)s * a.c.max_pages;
+    if (lo < hi) {
+      int s = from_seq[0];
+      Seq q{from_seq[1], from_seq[2], from_seq[3]};
+      int tiles = seq_tiles<C>(q), groups = seq_groups<C>(p, q);
+      int64_t seq_at = *from, pos = lo;
+      int unit = div_small(pos - seq_at, tiles);
+      if (p.align && seq_at + (int64_t)unit * tiles < pos) ++unit;         // the first unit that starts here
+      if (p.align) pos = seq_at + (int64_t)unit * tiles;
       const int nbox = C::TILE / p.box;
-      // page and slot of this lane's first box, one tile ahead of its use
-      auto lookup = [&](int tile, int b, int& page, int& off) {
-        const int tok = tile * C::TILE + b * p.box;
-        page = a.c.num_pages;                      // out of range: zero fill
-        off = 0;
-        if (tok < q.len && b < nbox) {
-          const int pg = __ldg(bt + tok / a.c.page_size);
-          off = tok % a.c.page_size;
-          if (pg >= 0 && pg < a.c.num_pages) page = pg;
-          else raise_error(a.err, kDevErrCache);
-        }
-      };
-      int page, off;
-      lookup(t0, lane, page, off);
-      for (int tile = t0; tile < t1; ++tile, ++it) {
-        int npage = 0, noff = 0;
-        if (tile + 1 < t1) lookup(tile + 1, lane, npage, noff);
-        const int st = it % C::STAGES;
-        ok = wait_bar(empty + st, ((it / C::STAGES) & 1) ^ 1, abort);
-        if (!ok) break;
-        uint8_t* kd = ring + st * 2 * kStageHalf;
-        if (lane == 0) tc::mbar_arrive_expect_tx(full + st, 2 * kStageHalf);
-        __syncwarp();
-        for (int b = lane; b < nbox; b += 32) {
-          if (b >= 32) lookup(tile, b, page, off);
-#pragma unroll
-          for (int cb = 0; cb < CB; ++cb) {
-            const int dst = cb * (C::TILE * 128) + b * p.box * (kStageHalf / C::TILE / CB);
-            tma_load_4d(kd + dst, &mk, full + st, cb * COLS, off, kvh, page);
-            tma_load_4d(kd + kStageHalf + dst, &mv, full + st, cb * COLS, off, kvh, page);
+      while (pos < hi) {
+        if (unit >= groups * a.Nkv) {
+          // the next sequence with work: the warp looks at 32 of them at a time
+          seq_at += (int64_t)tiles * groups * a.Nkv;
+          int base = s + 1;
+          uint32_t has = 0;
+          Seq c{0, 0, 0};
+          for (; base < a.num_seqs; base += 32) {
+            c = base + lane < a.num_seqs ? load_seq(a, base + lane) : Seq{0, 0, 0};
+            has = __ballot_sync(0xffffffffu, c.len > 0);
+            if (has != 0) break;
           }
+          if (has == 0) break;                     // (cannot be: pos < hi <= total)
+          const int w = __ffs(has) - 1;
+          s = base + w;
+          q.bos = __shfl_sync(0xffffffffu, c.bos, w);
+          q.n = __shfl_sync(0xffffffffu, c.n, w);
+          q.len = __shfl_sync(0xffffffffu, c.len, w);
+          tiles = seq_tiles<C>(q);
+          groups = seq_groups<C>(p, q);
+          unit = 0;
+          continue;
         }
-        page = npage;
-        off = noff;
+        const int t0 = (int)(pos - seq_at - (int64_t)unit * tiles);
+        const int t1 = p.align ? tiles : (int)min((int64_t)tiles, t0 + (hi - pos));
+        const int kvh = unit / groups, x0 = (unit % groups) * NT;
+        const int nvalid = min(NT, q.n * p.NG - x0);
+        const int32_t* bt = a.c.bt + (int64_t)s * a.c.max_pages;
+        // page and slot of this lane's first box, one tile ahead of its use
+        auto lookup = [&](int tile, int b, int& page, int& off) {
+          const int tok = tile * C::TILE + b * p.box;
+          page = a.c.num_pages;                    // out of range: zero fill
+          off = 0;
+          if (tok < q.len && b < nbox) {
+            const int at = (int)((uint32_t)tok / (uint32_t)a.c.page_size);
+            const int pg = __ldg(bt + at);
+            off = tok - at * a.c.page_size;
+            if (pg >= 0 && pg < a.c.num_pages) page = pg;
+            else raise_error(a.err, kDevErrCache);
+          }
+        };
+        int page, off;
+        lookup(t0, lane, page, off);
+        ok = wait_bar(qempty, (npiece & 1) ^ 1, abort);
+        if (!ok) break;
+        // query rows: octet x of the sequence is token x / NG, heads (x % NG) * 8 .. of the kv head's G
+        int rows = 0;
+        for (int r = lane; r < nvalid * 8; r += 32) rows += (x0 + r / 8) % p.NG * 8 + r % 8 < p.G;
+        rows = __reduce_add_sync(0xffffffffu, rows);
+        if (lane == 0) {
+          Piece d;
+          d.tile0 = t0; d.tile1 = t1;
+          d.slot = t0 == 0 && t1 == tiles ? -1 : 2 * (int)blockIdx.x + (t0 == 0 ? 1 : 0);
+          d.len = q.len; d.n = q.n; d.bos = q.bos; d.x0 = x0; d.nvalid = nvalid; d.kvh = kvh;
+          *piece = d;
+          if (t0 == 0 && t1 < tiles)
+            rec = {1, q.bos, x0, nvalid, kvh, rg.before(pos + tiles) - (int)blockIdx.x};
+          tc::mbar_arrive_expect_tx(qfull, (uint32_t)(rows * D * sizeof(T)));
+        }
+        __syncwarp();
+        for (int r = lane; r < nvalid * 8; r += 32) {
+          const int x = x0 + r / 8, h = x % p.NG * 8 + r % 8;
+          if (h < p.G)
+            tc::bulk_load(qs + r * C::QPITCH,
+                          static_cast<const T*>(a.q.p) + (q.bos + x / p.NG) * a.q.ts + (kvh * p.G + h) * a.q.hs,
+                          D * sizeof(T), qfull);
+        }
+        ++npiece;
+        for (int tile = t0; tile < t1; ++tile, ++it) {
+          int npage = 0, noff = 0;
+          if (tile + 1 < t1) lookup(tile + 1, lane, npage, noff);
+          const int st = it % C::STAGES;
+          ok = wait_bar(empty + st, ((it / C::STAGES) & 1) ^ 1, abort);
+          if (!ok) break;
+          uint8_t* kd = ring + st * 2 * kStageHalf;
+          if (lane == 0) tc::mbar_arrive_expect_tx(full + st, 2 * kStageHalf);
+          __syncwarp();
+          for (int b = lane; b < nbox; b += 32) {
+            if (b >= 32) lookup(tile, b, page, off);
+#pragma unroll
+            for (int cb = 0; cb < CB; ++cb) {
+              const int dst = cb * (C::TILE * 128) + b * p.box * (kStageHalf / C::TILE / CB);
+              tma_load_4d(kd + dst, &mk, full + st, cb * COLS, off, kvh, page);
+              tma_load_4d(kd + kStageHalf + dst, &mv, full + st, cb * COLS, off, kvh, page);
+            }
+          }
+          page = npage;
+          off = noff;
+        }
+        if (!ok) break;
+        pos += t1 - t0;
+        ++unit;
       }
-      pos += t1 - t0;
     }
     if (ok) {
-      const int qslot = npiece & 1;
-      ok = wait_bar(qempty + qslot, ((npiece >> 1) & 1) ^ 1, abort);
+      ok = wait_bar(qempty, (npiece & 1) ^ 1, abort);
       if (ok && lane == 0) {
-        piece[qslot].tile0 = -1;
-        tc::mbar_arrive(qfull + qslot);
+        piece->tile0 = -1;
+        tc::mbar_arrive(qfull);
       }
     }
     if (lane == 0 && !p.align) p.rec[blockIdx.x] = rec;
@@ -699,11 +760,9 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
         raise_error(a.err, kDevErrTimeout);
       }
       // copies in flight land before the CTA's shared memory goes
-      const int zero = 0;
-      for (int i = max(0, it - C::STAGES); i < it; ++i)
-        wait_bar(full + i % C::STAGES, (i / C::STAGES) & 1, const_cast<volatile int*>(&zero));
-      for (int i = max(0, npiece - 2); i < npiece; ++i)
-        wait_bar(qfull + (i & 1), (i >> 1) & 1, const_cast<volatile int*>(&zero));
+      int none = 0;
+      for (int i = max(0, it - C::STAGES); i < it; ++i) wait_bar(full + i % C::STAGES, (i / C::STAGES) & 1, &none);
+      if (npiece > 0) wait_bar(qfull, (npiece - 1) & 1, &none);
     }
     return;
   }
@@ -724,81 +783,82 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
   const int tw = warp % C::TG;                     // which slices; warps tw + k TG share them
   typename WarpOf<T, D, NT>::type w;
   int it = 0;
+  // After a wait that ran out a warp carries on with what the stages hold until the next
+  // barrier of all consumers, where they agree to stop: no barrier is left short of a warp.
   for (int np = 0;; ++np) {
-    const int qslot = np & 1;
-    bool ok = wait_bar(qfull + qslot, (np >> 1) & 1, abort);
-    Piece d{};
-    if (ok) {
-      d = piece[qslot];
-      if (d.tile0 < 0) break;
-      w.start(qs + qslot * C::QBYTES, warp / C::TG, lane);
-      auto lim = [&](int nt) { return d.len - d.n + (d.x0 + min(nt, d.nvalid - 1)) / p.NG + 1; };
-      const int most = lim(NT - 1);
-      for (int tile = d.tile0; tile < d.tile1; ++tile, ++it) {
-        int j = C::SL >= C::TG ? tw : tw - (it * C::SL) % C::TG;           // this warp's first slice of the stage
-        if (j < 0 || j >= C::SL) continue;
-        const int st = it % C::STAGES;
-        if (!wait_bar(full + st, (it / C::STAGES) & 1, abort)) {
-          ok = false;
-          break;
+    bool ok = wait_bar(qfull, np & 1, abort);
+    if (tc::named_sync_or(1, C::CW * 32, !ok)) {
+      if (lane == 0) {
+        *abort = 1;
+        raise_error(a.err, kDevErrTimeout);
+      }
+      break;
+    }
+    const Piece d = *piece;
+    if (d.tile0 < 0) break;
+    w.start(qs, warp / C::TG, xs + tw * 2 * (C::XW + C::XA), lane);
+    __syncwarp();
+    if (lane == 0) tc::mbar_arrive(qempty);
+    auto lim = [&](int nt) { return d.len - d.n + (d.x0 + min(nt, d.nvalid - 1)) / p.NG + 1; };
+    const int most = lim(NT - 1);
+    bool any = false;
+    for (int tile = d.tile0; tile < d.tile1; ++tile, ++it) {
+      int j = C::SL >= C::TG ? tw : tw - (it * C::SL) % C::TG;             // this warp's first slice of the stage
+      if (j < 0 || j >= C::SL) continue;
+      const int st = it % C::STAGES;
+      if (!wait_bar(full + st, (it / C::STAGES) & 1, abort)) {
+        ok = false;
+        if (lane == 0) *abort = 1;                 // ends the waits that follow at once
+      }
+      uint8_t* kd = ring + st * 2 * kStageHalf;
+      for (; j < C::SL; j += C::TG) {
+        const int tok0 = tile * C::TILE + j * C::SLICE;
+        if (tok0 < most) {
+          w.slice(kd, kd + kStageHalf, j * C::SLICE, tok0, d.nvalid, p.c, lim, tw, lane);
+          any = true;
         }
-        uint8_t* kd = ring + st * 2 * kStageHalf;
-        for (; j < C::SL; j += C::TG) {
-          const int tok0 = tile * C::TILE + j * C::SLICE;
-          if (tok0 < most) w.slice(kd, kd + kStageHalf, j * C::SLICE, tok0, d.nvalid, p.c, lim, lane);
-        }
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(empty + st);
+      }
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(empty + st);
+    }
+    // the warps' shares joined
+    w.give(jo + tw * C::ROWS * C::JP, jm + tw * C::ROWS, jl + tw * C::ROWS, any, lane);
+    if (tc::named_sync_or(1, C::CW * 32, !ok)) {
+      if (lane == 0) {
+        *abort = 1;
+        raise_error(a.err, kDevErrTimeout);
+      }
+      break;
+    }
+    for (int i = tid; i < d.nvalid * 8 * (D / 4); i += C::CW * 32) {
+      const int r = i / (D / 4), e = (i % (D / 4)) * 4;
+      const int x = d.x0 + r / 8, h = x % p.NG * 8 + r % 8;
+      if (h >= p.G) continue;
+      float mt = -INFINITY, lt = 0.f, y[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int k = 0; k < C::TG; ++k) mt = fmaxf(mt, jm[k * C::ROWS + r]);
+#pragma unroll
+      for (int k = 0; k < C::TG; ++k) {
+        const float mk_ = jm[k * C::ROWS + r];
+        if (mk_ == -INFINITY) continue;            // nothing in there (a row without slices is not written)
+        const float f = exp2f(mk_ - mt);
+        const float4 v = *reinterpret_cast<const float4*>(jo + (k * C::ROWS + r) * C::JP + e);
+        lt = fmaf(jl[k * C::ROWS + r], f, lt);
+        y[0] = fmaf(v.x, f, y[0]); y[1] = fmaf(v.y, f, y[1]);
+        y[2] = fmaf(v.z, f, y[2]); y[3] = fmaf(v.w, f, y[3]);
+      }
+      if (d.slot < 0) {
+        const float inv = lt == 0.f ? 0.f : 1.f / lt;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) y[k] *= inv;
+        finish4<T>(a, d.bos + x / p.NG, d.kvh * p.G + h, e, D, y);
+      } else {
+        const int64_t at = (int64_t)d.slot * C::ROWS + r;
+        store4(p.part_o + at * D + e, y);
+        if (e == 0) *reinterpret_cast<float2*>(p.part_ml + at * 2) = make_float2(mt, lt);
       }
     }
-    if (!ok && lane == 0) {
-      *abort = 1;
-      raise_error(a.err, kDevErrTimeout);
-    }
-    // the warps' shares joined, octet by octet
-    bool quit = false;
-    for (int nt = 0; nt < NT; ++nt) {
-      if (nt > 0 && nt >= d.nvalid) break;
-      if (ok) {
-#pragma unroll
-        for (int k = 0; k < NT; ++k)
-          if (k == nt) w.give(k, jo + tw * 8 * C::JP, jm + tw * 8, jl + tw * 8, lane);
-      }
-      if (tc::named_sync_or(1, C::CW * 32, !ok)) {
-        quit = true;
-        break;
-      }
-      const int x = d.x0 + nt, oct = x % p.NG;
-      for (int i = tid; i < 8 * (D / 4); i += C::CW * 32) {
-        const int h = i / (D / 4), e = (i % (D / 4)) * 4;
-        if (oct * 8 + h >= p.G) break;
-        float mt = -INFINITY, lt = 0.f, y[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int k = 0; k < C::TG; ++k) mt = fmaxf(mt, jm[k * 8 + h]);
-        const float base = mt == -INFINITY ? 0.f : mt;
-#pragma unroll
-        for (int k = 0; k < C::TG; ++k) {
-          const float f = exp2f(jm[k * 8 + h] - base);
-          const float4 v = *reinterpret_cast<const float4*>(jo + (k * 8 + h) * C::JP + e);
-          lt = fmaf(jl[k * 8 + h], f, lt);
-          y[0] = fmaf(v.x, f, y[0]); y[1] = fmaf(v.y, f, y[1]);
-          y[2] = fmaf(v.z, f, y[2]); y[3] = fmaf(v.w, f, y[3]);
-        }
-        if (d.slot < 0) {
-          const float inv = lt == 0.f ? 0.f : 1.f / lt;
-#pragma unroll
-          for (int k = 0; k < 4; ++k) y[k] *= inv;
-          finish4<T>(a, d.bos + x / p.NG, d.kvh * p.G + oct * 8 + h, e, D, y);
-        } else {
-          const int64_t r = (int64_t)d.slot * C::ROWS + nt * 8 + h;
-          store4(p.part_o + r * D + e, y);
-          if (e == 0) *reinterpret_cast<float2*>(p.part_ml + r * 2) = make_float2(mt, lt);
-        }
-      }
-      tc::named_sync(1, C::CW * 32);
-    }
-    if (quit) break;
-    if (lane == 0) tc::mbar_arrive(qempty + qslot);
+    tc::named_sync(1, C::CW * 32);
   }
 }
 
@@ -818,22 +878,30 @@ paged_attn_join_kernel(const __grid_constant__ Params p) {
   const SplitRec r = p.rec[blockIdx.x];
   const int row = blockIdx.y, x = r.x0 + row / 8, h = (x % p.NG) * 8 + row % 8;
   if (!r.valid || row >= r.nvalid * 8 || h >= p.G) return;
-  // CTA c0's last piece, then the first one of every CTA whose range starts before the unit's end
-  const int c0 = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int n = (int)((r.end * r.geff + r.total - 1) / r.total) - c0;
-  auto at = [&](int i) { return ((int64_t)2 * (c0 + i) + (i == 0 ? 1 : 0)) * (gridDim.y) + row; };
-  float2 ml = make_float2(-INFINITY, 0.f);
-  if (tid < n) ml = *reinterpret_cast<const float2*>(p.part_ml + at(tid) * 2);
-  float m = ml.x;
+  // CTA c0's last piece, then the first one of the CTAs behind it
+  const int c0 = blockIdx.x, n = r.pieces, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  auto at = [&](int i) { return ((int64_t)2 * (c0 + i) + (i == 0 ? 1 : 0)) * gridDim.y + row; };
+  float2 ml[kMaxCtas / kJoinThreads];
+  float m = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < kMaxCtas / kJoinThreads; ++i) {
+    const int j = tid + i * kJoinThreads;
+    ml[i] = j < n ? *reinterpret_cast<const float2*>(p.part_ml + at(j) * 2) : make_float2(-INFINITY, 0.f);
+    m = fmaxf(m, ml[i].x);
+  }
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
   if (lane == 0) red[0][warp] = m;
   __syncthreads();
 #pragma unroll
   for (int i = 0; i < kJoinThreads / 32; ++i) m = fmaxf(m, red[0][i]);
-  const float w = exp2f(ml.x - (m == -INFINITY ? 0.f : m));
-  float l = w * ml.y;
-  if (tid < n) sw[tid] = w;
+  float l = 0.f;
+#pragma unroll
+  for (int i = 0; i < kMaxCtas / kJoinThreads; ++i) {
+    const float w = exp2f(ml[i].x - (m == -INFINITY ? 0.f : m));
+    l = fmaf(w, ml[i].y, l);
+    sw[tid + i * kJoinThreads] = w;
+  }
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
   if (lane == 0) red[1][warp] = l;
@@ -903,7 +971,7 @@ cudaError_t launch_c(const PagedAttnArgs& a, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < 64) ready[dev] = true;
   }
-  const int grid = std::min(num_sms(), kMaxCtas);
+  const int grid = std::min(kOcc * num_sms(), kMaxCtas);
   Params p{};
   p.a = a;
   p.G = a.Nq / a.Nkv;
@@ -947,7 +1015,7 @@ cudaError_t launch_bf16(const PagedAttnArgs& a, int nt, cudaStream_t s) {
 size_t paged_attn_workspace_bytes(int num_seqs, int total, int Nq, int Nkv, int D) {
   // the same for every type and table: the caller may size it before those are known
   const int rows = octets_per_pass(num_seqs, total, Nq, Nkv, D, true) * 8;
-  const size_t grid = std::min(num_sms(), kMaxCtas);
+  const size_t grid = std::min(kOcc * num_sms(), kMaxCtas);
   return align16(sizeof(SplitRec) * grid) + align16(2 * grid * rows * 2 * 4) + 2 * grid * rows * D * 4;
 }
 
