@@ -94,25 +94,38 @@ struct SplitRec {
   int pieces;              // CTAs c .. c + pieces - 1 hold its pieces
 };
 
+__device__ __noinline__ int64_t div_long(int64_t x, int64_t d) { return x / d; }
+// x / d for x / d < 2^31, by the short division where x allows it.
+__device__ __forceinline__ int div_small(int64_t x, int d) {
+  return x >> 32 ? (int)div_long(x, d) : (int)((uint32_t)x / (uint32_t)d);
+}
+
 // Bounds of the ranges: CTA c of n takes [at(c), at(c + 1)) of `total` tiles.
 struct Ranges {
   int64_t q;
   int r, n;
   __device__ __forceinline__ Ranges(int64_t total, int ctas) : n(ctas) {
-    if (total >> 31) {
-      q = total / ctas;
-      r = (int)(total % ctas);
-    } else {
-      q = (uint32_t)total / (uint32_t)ctas;
-      r = (int)((uint32_t)total - (uint32_t)q * (uint32_t)ctas);
-    }
+    q = total >> 32 ? div_long(total, ctas) : (uint32_t)total / (uint32_t)ctas;
+    r = (int)(total - q * ctas);
   }
   __device__ __forceinline__ int64_t at(int c) const { return q * c + min(c, r); }
   // CTAs that start before position `end` > 0
   __device__ __forceinline__ int before(int64_t end) const {
     const int64_t wide = (q + 1) * r;
-    return end <= wide ? (int)((end + q) / (q + 1)) : r + (int)((end - wide + q - 1) / q);
+    return end <= wide ? (int)div_long(end + q, q + 1) : r + (int)div_long(end - wide + q - 1, q);
   }
+};
+
+// x / d for 0 <= x < 2^31 by one multiplication (d > 0): with 2^k the first power of two that is
+// at least d and m = floor(2^32 (2^k - d) / d) + 1, x / d = (hi32(x m) + x) >> k.
+struct Div {
+  uint32_t d, m, k;
+  static Div of(uint32_t d) {
+    uint32_t k = 0;
+    while ((uint64_t)1 << k < d) ++k;
+    return {d, (uint32_t)(((((uint64_t)1 << k) - d) << 32) / d + 1), k};
+  }
+  __device__ __forceinline__ int quot(int x) const { return (int)((__umulhi((uint32_t)x, m) + (uint32_t)x) >> k); }
 };
 
 __host__ __device__ constexpr size_t align16(size_t x) { return (x + 15) & ~(size_t)15; }
@@ -120,6 +133,7 @@ __host__ __device__ constexpr size_t align16(size_t x) { return (x + 15) & ~(siz
 struct Params {
   PagedAttnArgs a;
   int G, NG;               // query heads per kv head, octets per token
+  Div by_NG, by_page;
   int box, align;          // slots per TMA box; ranges end at unit borders
   float c;                 // scale * log2(e)
   SplitRec* rec;           // [grid]
@@ -134,18 +148,37 @@ __device__ __forceinline__ uint64_t now_ns() {
   return t;
 }
 
+// Kernels of a few us run their code about once: what is not on the common path is kept out
+// of line, since every line of code that is fetched on the way costs time.
+
 // Bounded wait of a whole warp on a phase; gives up when another warp aborted or the time
 // ran out, all lanes alike.
+__device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  const uint64_t t0 = now_ns();
+#pragma unroll 1
+  for (uint32_t i = 0; i < kPollCap; ++i) {
+    if (tc::mbar_try_wait(bar, parity)) return true;
+    if (*abort != 0 || now_ns() - t0 > kWaitNs) break;
+  }
+  return false;
+}
 __device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, volatile int* abort) {
   bool ok = tc::mbar_try_wait(bar, parity);
-  if (!ok) {
-    const uint64_t t0 = now_ns();
-    for (uint32_t i = 0; i < kPollCap && !ok; ++i) {
-      ok = tc::mbar_try_wait(bar, parity);
-      if (*abort != 0 || now_ns() - t0 > kWaitNs) break;
-    }
-  }
+  if (!ok) ok = wait_slow(bar, parity, abort);
   return __all_sync(0xffffffffu, ok);
+}
+
+// 2^x and 1 / x by the hardware's approximations (2^-22 and 2^-23 relative; results below
+// 2^-126 become 0, -inf gives 0).
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
 
 // One box of the 4-D map {D, slot, kv head, page}.
@@ -195,10 +228,6 @@ __device__ __forceinline__ Seq load_seq(const PagedAttnArgs& a, int s, int* err 
   if (!ok && err != nullptr) raise_error(err, kDevErrSeqlens);
   return {bos, n, n > 0 ? len : 0};
 }
-// x / d for 0 <= x / d < 2^31, by the short division where x allows it.
-__device__ __forceinline__ int div_small(int64_t x, int d) {
-  return x >> 32 ? (int)(x / d) : (int)((uint32_t)x / (uint32_t)d);
-}
 template <typename C>
 __device__ __forceinline__ int seq_tiles(const Seq& q) { return (q.len + C::TILE - 1) / C::TILE; }
 template <typename C>
@@ -211,14 +240,45 @@ __device__ __forceinline__ int64_t seq_work(const Params& p, const Seq& q) {
   return q.len == 0 ? 0 : (int64_t)seq_tiles<C>(q) * seq_groups<C>(p, q) * p.a.Nkv;
 }
 
-// y = o * sigmoid(gate), four elements of (token t, head h) from d.
+// The next sequence behind s with anything to attend (the warp looks at 32 at a time); its
+// index, num_seqs when there is none.
+__device__ __noinline__ int next_seq(const PagedAttnArgs& a, int s, Seq* q) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll 1
+  for (int base = s + 1; base < a.num_seqs; base += 32) {
+    const Seq c = base + lane < a.num_seqs ? load_seq(a, base + lane) : Seq{0, 0, 0};
+    const uint32_t has = __ballot_sync(0xffffffffu, c.len > 0);
+    if (has != 0) {
+      const int w = __ffs(has) - 1;
+      q->bos = __shfl_sync(0xffffffffu, c.bos, w);
+      q->n = __shfl_sync(0xffffffffu, c.n, w);
+      q->len = __shfl_sync(0xffffffffu, c.len, w);
+      return base + w;
+    }
+  }
+  return a.num_seqs;
+}
+// The rows of a sequence with nothing to attend, by a warp.
+__device__ __noinline__ void zero_rows(const PagedAttnArgs& a, const Seq& q) {
+  const int64_t b = (int64_t)q.bos * a.Nq * a.D, e = b + (int64_t)q.n * a.Nq * a.D;
+  const float z[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+  for (int64_t i = b + (threadIdx.x & 31) * 4; i < e; i += 128) {
+    if (a.out_bf16) store4(static_cast<bf16*>(a.o) + i, z);
+    else store4(static_cast<float*>(a.o) + i, z);
+  }
+}
+
+// Four elements of (token t, head h) from d: the gate, and y = o * sigmoid(gate).
 template <typename T>
-__device__ __forceinline__ void finish4(const PagedAttnArgs& a, int t, int h, int d, int D, float (&y)[4]) {
+__device__ __forceinline__ void gate4(const PagedAttnArgs& a, int t, int h, int d, float (&g)[4]) {
+  if (a.gate.p != nullptr) load4(static_cast<const T*>(a.gate.p) + t * a.gate.ts + h * a.gate.hs + d, g);
+}
+__device__ __forceinline__ void finish4(const PagedAttnArgs& a, int t, int h, int d, int D, const float (&g)[4],
+                                        float (&y)[4]) {
   if (a.gate.p != nullptr) {
-    float g[4];
-    load4(static_cast<const T*>(a.gate.p) + t * a.gate.ts + h * a.gate.hs + d, g);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) y[i] *= sigmoidf_(g[i]);
+    for (int i = 0; i < 4; ++i) y[i] *= rcp(1.f + ex2(-kLog2e * g[i]));
   }
   const int64_t at = ((int64_t)t * a.Nq + h) * D + d;
   if (a.out_bf16) store4(static_cast<bf16*>(a.o) + at, y);
@@ -323,12 +383,12 @@ struct TcWarp {
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const float mn = fmaxf(m[k][e], mx[e]);
-        al[k][e] = mn == m[k][e] ? 1.f : exp2f(m[k][e] - mn);      // (-inf stays -inf: no change)
+        al[k][e] = mn == m[k][e] ? 1.f : ex2(m[k][e] - mn);      // (-inf stays -inf: no change)
         m[k][e] = mn;
       }
       const float b0 = m[k][0] == -INFINITY ? 0.f : m[k][0], b1 = m[k][1] == -INFINITY ? 0.f : m[k][1];
-      const float p0 = exp2f(s[k][0] - b0), p1 = exp2f(s[k][1] - b1);
-      const float p2 = exp2f(s[k][2] - b0), p3 = exp2f(s[k][3] - b1);
+      const float p0 = ex2(s[k][0] - b0), p1 = ex2(s[k][1] - b1);
+      const float p2 = ex2(s[k][2] - b0), p3 = ex2(s[k][3] - b1);
       l[k][0] = fmaf(l[k][0], al[k][0], p0 + p2);
       l[k][1] = fmaf(l[k][1], al[k][1], p1 + p3);
       const uint32_t h0 = pack_bf16(p0, p1), h1 = pack_bf16(p2, p3);
@@ -381,6 +441,7 @@ struct TcWarp {
     // Rows that an octet does not see may hold anything, and 0 * NaN is NaN: at the end of the
     // visible range they are cleared in the stage, in the columns that this warp reads.
     auto clear = [&](int last) {
+#pragma unroll 1
       for (int e = lane; e < (16 - last) * (2 * OS); e += 32) {
         const int r = j0 + last + e / (2 * OS), ch = 2 * d0 + e % (2 * OS);
         *reinterpret_cast<uint4*>(vs_ + (ch >> 3) * (C::TILE * 128) + r * 128 + ((ch & 7) << 4)) = make_uint4(0, 0, 0, 0);
@@ -512,7 +573,7 @@ struct SimtWarp {
     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
     if (__any_sync(0xffffffffu, mx > m)) {
       const float mn = fmaxf(m, mx);
-      const float al = mn == m ? 1.f : exp2f(m - mn);
+      const float al = mn == m ? 1.f : ex2(m - mn);
       m = mn;
       l *= al;
 #pragma unroll
@@ -522,7 +583,7 @@ struct SimtWarp {
         for (int e = 0; e < E; ++e) o[h][e] *= a;
       }
     }
-    const float p = exp2f(s - (m == -INFINITY ? 0.f : m));
+    const float p = ex2(s - (m == -INFINITY ? 0.f : m));
     l += p;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -586,6 +647,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
 
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (tid == C::CW * 32) {
+#pragma unroll 1
     for (int i = 0; i < C::STAGES; ++i) {
       tc::mbar_init(full + i, 1);
       tc::mbar_init(empty + i, C::USERS * C::DS);
@@ -601,6 +663,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
   const int per = (a.num_seqs + C::THREADS - 1) / C::THREADS;
   const int s_lo = min(a.num_seqs, tid * per), s_hi = min(a.num_seqs, s_lo + per);
   int64_t sum = 0;
+#pragma unroll 1
   for (int s = s_lo; s < s_hi; ++s) sum += seq_work<C>(p, load_seq(a, s));
   int64_t inc = sum;
 #pragma unroll
@@ -622,6 +685,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
   const int64_t hi = mine ? rg.at(blockIdx.x + 1) : total;
   if (before <= lo && lo < before + sum) {
     int64_t at = before;
+#pragma unroll 1
     for (int s = s_lo; s < s_hi; ++s) {
       const Seq q = load_seq(a, s);
       const int64_t w = seq_work<C>(p, q);
@@ -652,24 +716,12 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
       if (p.align && seq_at + (int64_t)unit * tiles < pos) ++unit;         // the first unit that starts here
       if (p.align) pos = seq_at + (int64_t)unit * tiles;
       const int nbox = C::TILE / p.box;
+#pragma unroll 1
       while (pos < hi) {
         if (unit >= groups * a.Nkv) {
-          // the next sequence with work: the warp looks at 32 of them at a time
           seq_at += (int64_t)tiles * groups * a.Nkv;
-          int base = s + 1;
-          uint32_t has = 0;
-          Seq c{0, 0, 0};
-          for (; base < a.num_seqs; base += 32) {
-            c = base + lane < a.num_seqs ? load_seq(a, base + lane) : Seq{0, 0, 0};
-            has = __ballot_sync(0xffffffffu, c.len > 0);
-            if (has != 0) break;
-          }
-          if (has == 0) break;                     // (cannot be: pos < hi <= total)
-          const int w = __ffs(has) - 1;
-          s = base + w;
-          q.bos = __shfl_sync(0xffffffffu, c.bos, w);
-          q.n = __shfl_sync(0xffffffffu, c.n, w);
-          q.len = __shfl_sync(0xffffffffu, c.len, w);
+          s = next_seq(a, s, &q);
+          if (s >= a.num_seqs) break;              // (cannot be: pos < hi <= total)
           tiles = seq_tiles<C>(q);
           groups = seq_groups<C>(p, q);
           unit = 0;
@@ -686,7 +738,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
           page = a.c.num_pages;                    // out of range: zero fill
           off = 0;
           if (tok < q.len && b < nbox) {
-            const int at = (int)((uint32_t)tok / (uint32_t)a.c.page_size);
+            const int at = p.by_page.quot(tok);
             const int pg = __ldg(bt + at);
             off = tok - at * a.c.page_size;
             if (pg >= 0 && pg < a.c.num_pages) page = pg;
@@ -695,40 +747,16 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
         };
         int page, off;
         lookup(t0, lane, page, off);
-        ok = wait_bar(qempty, (npiece & 1) ^ 1, abort);
-        if (!ok) break;
-        // query rows: octet x of the sequence is token x / NG, heads (x % NG) * 8 .. of the kv head's G
-        int rows = 0;
-        for (int r = lane; r < nvalid * 8; r += 32) rows += (x0 + r / 8) % p.NG * 8 + r % 8 < p.G;
-        rows = __reduce_add_sync(0xffffffffu, rows);
-        if (lane == 0) {
-          Piece d;
-          d.tile0 = t0; d.tile1 = t1;
-          d.slot = t0 == 0 && t1 == tiles ? -1 : 2 * (int)blockIdx.x + (t0 == 0 ? 1 : 0);
-          d.len = q.len; d.n = q.n; d.bos = q.bos; d.x0 = x0; d.nvalid = nvalid; d.kvh = kvh;
-          *piece = d;
-          if (t0 == 0 && t1 < tiles)
-            rec = {1, q.bos, x0, nvalid, kvh, rg.before(pos + tiles) - (int)blockIdx.x};
-          tc::mbar_arrive_expect_tx(qfull, (uint32_t)(rows * D * sizeof(T)));
-        }
-        __syncwarp();
-        for (int r = lane; r < nvalid * 8; r += 32) {
-          const int x = x0 + r / 8, h = x % p.NG * 8 + r % 8;
-          if (h < p.G)
-            tc::bulk_load(qs + r * C::QPITCH,
-                          static_cast<const T*>(a.q.p) + (q.bos + x / p.NG) * a.q.ts + (kvh * p.G + h) * a.q.hs,
-                          D * sizeof(T), qfull);
-        }
-        ++npiece;
+#pragma unroll 1
         for (int tile = t0; tile < t1; ++tile, ++it) {
           int npage = 0, noff = 0;
-          if (tile + 1 < t1) lookup(tile + 1, lane, npage, noff);
           const int st = it % C::STAGES;
           ok = wait_bar(empty + st, ((it / C::STAGES) & 1) ^ 1, abort);
           if (!ok) break;
           uint8_t* kd = ring + st * 2 * kStageHalf;
           if (lane == 0) tc::mbar_arrive_expect_tx(full + st, 2 * kStageHalf);
           __syncwarp();
+#pragma unroll 1
           for (int b = lane; b < nbox; b += 32) {
             if (b >= 32) lookup(tile, b, page, off);
 #pragma unroll
@@ -738,8 +766,54 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
               tma_load_4d(kd + kStageHalf + dst, &mv, full + st, cb * COLS, off, kvh, page);
             }
           }
+          if (tile + 1 < t1) lookup(tile + 1, lane, npage, noff);
           page = npage;
           off = noff;
+          if (tile != t0) continue;
+          // behind its first tile: the piece and its query rows.  Octet x of the sequence is token
+          // x / NG, heads (x % NG) * 8 .. of the kv head's G
+          ok = wait_bar(qempty, (npiece & 1) ^ 1, abort);
+          if (!ok) {
+            ++it;                                  // (this tile is in flight)
+            break;
+          }
+          int rows = 0;
+          auto head_of = [&](int r, int& tok) {    // head within the kv head's, and token, of row r
+            const int x = x0 + r / 8;
+            tok = p.by_NG.quot(x);
+            return (x - tok * p.NG) * 8 + r % 8;
+          };
+          int tok;
+#pragma unroll 1
+          for (int r = lane; r < nvalid * 8; r += 32) rows += head_of(r, tok) < p.G;
+          rows = __reduce_add_sync(0xffffffffu, rows);
+          if (lane == 0) {
+            Piece d;
+            d.tile0 = t0; d.tile1 = t1;
+            d.slot = t0 == 0 && t1 == tiles ? -1 : 2 * (int)blockIdx.x + (t0 == 0 ? 1 : 0);
+            d.len = q.len; d.n = q.n; d.bos = q.bos; d.x0 = x0; d.nvalid = nvalid; d.kvh = kvh;
+            *piece = d;
+            if (t0 == 0 && t1 < tiles)
+              rec = {1, q.bos, x0, nvalid, kvh, rg.before(pos + tiles) - (int)blockIdx.x};
+            tc::mbar_arrive_expect_tx(qfull, (uint32_t)(rows * D * sizeof(T)));
+          }
+          __syncwarp();
+#pragma unroll 1
+          for (int r = lane; r < nvalid * 8; r += 32) {
+            const int h = head_of(r, tok);
+            if (h < p.G) {
+              tc::bulk_load(qs + r * C::QPITCH,
+                            static_cast<const T*>(a.q.p) + (q.bos + tok) * a.q.ts + (kvh * p.G + h) * a.q.hs,
+                            D * sizeof(T), qfull);
+              if (a.gate.p != nullptr && t1 - t0 == tiles) {   // needed at the end of the piece
+                const T* gp = static_cast<const T*>(a.gate.p) + (q.bos + tok) * a.gate.ts + (kvh * p.G + h) * a.gate.hs;
+#pragma unroll 1
+                for (int i = 0; i < D; i += 128 / (int)sizeof(T))
+                  asm volatile("prefetch.global.L2 [%0];" ::"l"(gp + i));
+              }
+            }
+          }
+          ++npiece;
         }
         if (!ok) break;
         pos += t1 - t0;
@@ -761,6 +835,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
       }
       // copies in flight land before the CTA's shared memory goes
       int none = 0;
+#pragma unroll 1
       for (int i = max(0, it - C::STAGES); i < it; ++i) wait_bar(full + i % C::STAGES, (i / C::STAGES) & 1, &none);
       if (npiece > 0) wait_bar(qfull, (npiece - 1) & 1, &none);
     }
@@ -769,22 +844,17 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
 
   // -------------------------------------------------------------- consumers
   // sequences with nothing to attend: their rows are zero; every sequence's metadata is checked once
+#pragma unroll 1
   for (int s = blockIdx.x * C::CW + warp; s < a.num_seqs; s += gridDim.x * C::CW) {
     const Seq q = load_seq(a, s, lane == 0 ? a.err : nullptr);
-    if (q.n > 0 && q.len == 0) {
-      const int64_t b = (int64_t)q.bos * a.Nq * D, e = b + (int64_t)q.n * a.Nq * D;
-      const float z[4] = {0.f, 0.f, 0.f, 0.f};
-      for (int64_t i = b + lane * 4; i < e; i += 128) {
-        if (a.out_bf16) store4(static_cast<bf16*>(a.o) + i, z);
-        else store4(static_cast<float*>(a.o) + i, z);
-      }
-    }
+    if (q.n > 0 && q.len == 0) zero_rows(a, q);
   }
   const int tw = warp % C::TG;                     // which slices; warps tw + k TG share them
   typename WarpOf<T, D, NT>::type w;
   int it = 0;
   // After a wait that ran out a warp carries on with what the stages hold until the next
   // barrier of all consumers, where they agree to stop: no barrier is left short of a warp.
+#pragma unroll 1
   for (int np = 0;; ++np) {
     bool ok = wait_bar(qfull, np & 1, abort);
     if (tc::named_sync_or(1, C::CW * 32, !ok)) {
@@ -799,9 +869,10 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
     w.start(qs, warp / C::TG, xs + tw * 2 * (C::XW + C::XA), lane);
     __syncwarp();
     if (lane == 0) tc::mbar_arrive(qempty);
-    auto lim = [&](int nt) { return d.len - d.n + (d.x0 + min(nt, d.nvalid - 1)) / p.NG + 1; };
+    auto lim = [&](int nt) { return d.len - d.n + p.by_NG.quot(d.x0 + min(nt, d.nvalid - 1)) + 1; };
     const int most = lim(NT - 1);
     bool any = false;
+#pragma unroll 1
     for (int tile = d.tile0; tile < d.tile1; ++tile, ++it) {
       int j = C::SL >= C::TG ? tw : tw - (it * C::SL) % C::TG;             // this warp's first slice of the stage
       if (j < 0 || j >= C::SL) continue;
@@ -811,6 +882,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
         if (lane == 0) *abort = 1;                 // ends the waits that follow at once
       }
       uint8_t* kd = ring + st * 2 * kStageHalf;
+#pragma unroll 1
       for (; j < C::SL; j += C::TG) {
         const int tok0 = tile * C::TILE + j * C::SLICE;
         if (tok0 < most) {
@@ -830,106 +902,194 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
       }
       break;
     }
-    for (int i = tid; i < d.nvalid * 8 * (D / 4); i += C::CW * 32) {
+    // four columns per thread at a time, the next ones' gates loaded ahead
+    const int groups4 = d.nvalid * 8 * (D / 4);
+    auto place = [&](int i, int& tok) {            // head of group i (-1: no such row), and token
+      const int r = i / (D / 4), x = d.x0 + r / 8, t = p.by_NG.quot(x), h = (x - t * p.NG) * 8 + r % 8;
+      tok = d.bos + t;
+      return i < groups4 && h < p.G ? d.kvh * p.G + h : -1;
+    };
+    int tok, hd = place(tid, tok);
+    float gt[4];
+    if (hd >= 0 && d.slot < 0) gate4<T>(a, tok, hd, tid % (D / 4) * 4, gt);
+#pragma unroll 1
+    for (int i = tid; i < groups4; i += C::CW * 32) {
       const int r = i / (D / 4), e = (i % (D / 4)) * 4;
-      const int x = d.x0 + r / 8, h = x % p.NG * 8 + r % 8;
-      if (h >= p.G) continue;
-      float mt = -INFINITY, lt = 0.f, y[4] = {0.f, 0.f, 0.f, 0.f};
+      int ntok, nhd = place(i + C::CW * 32, ntok);
+      float ngt[4];
+      if (nhd >= 0 && d.slot < 0) gate4<T>(a, ntok, nhd, (i + C::CW * 32) % (D / 4) * 4, ngt);
+      if (hd >= 0) {
+        float mt = -INFINITY, lt = 0.f, y[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int k = 0; k < C::TG; ++k) mt = fmaxf(mt, jm[k * C::ROWS + r]);
+        for (int k = 0; k < C::TG; ++k) mt = fmaxf(mt, jm[k * C::ROWS + r]);
 #pragma unroll
-      for (int k = 0; k < C::TG; ++k) {
-        const float mk_ = jm[k * C::ROWS + r];
-        if (mk_ == -INFINITY) continue;            // nothing in there (a row without slices is not written)
-        const float f = exp2f(mk_ - mt);
-        const float4 v = *reinterpret_cast<const float4*>(jo + (k * C::ROWS + r) * C::JP + e);
-        lt = fmaf(jl[k * C::ROWS + r], f, lt);
-        y[0] = fmaf(v.x, f, y[0]); y[1] = fmaf(v.y, f, y[1]);
-        y[2] = fmaf(v.z, f, y[2]); y[3] = fmaf(v.w, f, y[3]);
+        for (int k = 0; k < C::TG; ++k) {
+          const float mk_ = jm[k * C::ROWS + r];
+          if (mk_ == -INFINITY) continue;          // nothing in there (a row without slices is not written)
+          const float f = ex2(mk_ - mt);
+          const float4 v = *reinterpret_cast<const float4*>(jo + (k * C::ROWS + r) * C::JP + e);
+          lt = fmaf(jl[k * C::ROWS + r], f, lt);
+          y[0] = fmaf(v.x, f, y[0]); y[1] = fmaf(v.y, f, y[1]);
+          y[2] = fmaf(v.z, f, y[2]); y[3] = fmaf(v.w, f, y[3]);
+        }
+        if (d.slot < 0) {
+          const float inv = lt == 0.f ? 0.f : rcp(lt);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) y[k] *= inv;
+          finish4(a, tok, hd, e, D, gt, y);
+        } else {
+          const int64_t at = (int64_t)d.slot * C::ROWS + r;
+          store4(p.part_o + at * D + e, y);
+          if (e == 0) *reinterpret_cast<float2*>(p.part_ml + at * 2) = make_float2(mt, lt);
+        }
       }
-      if (d.slot < 0) {
-        const float inv = lt == 0.f ? 0.f : 1.f / lt;
+      tok = ntok;
+      hd = nhd;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) y[k] *= inv;
-        finish4<T>(a, d.bos + x / p.NG, d.kvh * p.G + h, e, D, y);
-      } else {
-        const int64_t at = (int64_t)d.slot * C::ROWS + r;
-        store4(p.part_o + at * D + e, y);
-        if (e == 0) *reinterpret_cast<float2*>(p.part_ml + at * 2) = make_float2(mt, lt);
-      }
+      for (int k = 0; k < 4; ++k) gt[k] = ngt[k];
     }
     tc::named_sync(1, C::CW * 32);
   }
 }
 
 // ------------------------------------------------------------------ the join
-// Block (c, row) joins one row of the unit that starts in CTA c's range and ends behind it,
-// its pieces in order.  All loads of a block but the record are independent: first the
-// maxima and sums (a thread per piece) for the weights, beside them the outputs, NP pieces
-// at a time.  Launched while the main kernel runs; the first step is to wait for its end.
+// Launched while the main kernel runs; the first step is to wait for its end.  Two forms,
+// so that neither many cut units start blocks for nothing nor a long one is joined by few.
+//
+// Many units (so few pieces each): block (c, y) joins the unit that starts in CTA c's range
+// and ends behind it, if there is one; a thread takes four columns of a row, piece by piece.
 constexpr int kJoinThreads = 256;
+__device__ __forceinline__ int64_t piece_row(int c0, int i, int rows, int row) {
+  // CTA c0's last piece (slot 2 c0 + 1), then the first ones of the CTAs behind it
+  return ((int64_t)2 * (c0 + i) + (i == 0 ? 1 : 0)) * rows + row;
+}
 template <typename T, int D>
 __global__ void __launch_bounds__(kJoinThreads)
-paged_attn_join_kernel(const __grid_constant__ Params p) {
-  constexpr int LPR = D / 4;                       // threads across a row
-  constexpr int NP = kJoinThreads / LPR;           // pieces in flight
-  __shared__ float sw[kMaxCtas], so[NP][D], red[2][kJoinThreads / 32];
+paged_attn_join_kernel(const __grid_constant__ Params p, int rows) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const SplitRec r = p.rec[blockIdx.x];
-  const int row = blockIdx.y, x = r.x0 + row / 8, h = (x % p.NG) * 8 + row % 8;
-  if (!r.valid || row >= r.nvalid * 8 || h >= p.G) return;
-  // CTA c0's last piece, then the first one of the CTAs behind it
-  const int c0 = blockIdx.x, n = r.pieces, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  auto at = [&](int i) { return ((int64_t)2 * (c0 + i) + (i == 0 ? 1 : 0)) * gridDim.y + row; };
-  float2 ml[kMaxCtas / kJoinThreads];
-  float m = -INFINITY;
+  if (!r.valid) return;
+#pragma unroll 1
+  for (int i = blockIdx.y * kJoinThreads + threadIdx.x; i < r.nvalid * 8 * (D / 4); i += gridDim.y * kJoinThreads) {
+    const int row = i / (D / 4), e = (i % (D / 4)) * 4;
+    const int x = r.x0 + row / 8, t = p.by_NG.quot(x), h = (x - t * p.NG) * 8 + row % 8;
+    if (h >= p.G) continue;
+    float gt[4], m = -INFINITY, l = 0.f, y[4] = {0.f, 0.f, 0.f, 0.f};
+    gate4<T>(p.a, r.bos + t, r.kvh * p.G + h, e, gt);
+#pragma unroll 1
+    for (int j0 = 0; j0 < r.pieces; j0 += 4) {
+      float2 ml[4];
+      float v[4][4];
 #pragma unroll
-  for (int i = 0; i < kMaxCtas / kJoinThreads; ++i) {
-    const int j = tid + i * kJoinThreads;
-    ml[i] = j < n ? *reinterpret_cast<const float2*>(p.part_ml + at(j) * 2) : make_float2(-INFINITY, 0.f);
-    m = fmaxf(m, ml[i].x);
+      for (int j = 0; j < 4; ++j) {
+        ml[j] = make_float2(-INFINITY, 0.f);
+        if (j0 + j < r.pieces) {
+          const int64_t at = piece_row(blockIdx.x, j0 + j, rows, row);
+          ml[j] = *reinterpret_cast<const float2*>(p.part_ml + at * 2);
+          load4(p.part_o + at * D + e, v[j]);
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (j0 + j >= r.pieces) break;
+        const float mn = fmaxf(m, ml[j].x), base = mn == -INFINITY ? 0.f : mn;
+        const float f0 = ex2(m - base), f1 = ex2(ml[j].x - base);
+        l = l * f0 + ml[j].y * f1;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) y[k] = y[k] * f0 + v[j][k] * f1;
+        m = mn;
+      }
+    }
+    const float inv = l == 0.f ? 0.f : rcp(l);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) y[k] *= inv;
+    finish4(p.a, r.bos + t, r.kvh * p.G + h, e, D, gt, y);
   }
+}
+
+// Few units (so many pieces): block (u, row, z) joins 64 columns of a row of the u-th CTA
+// with a record.  All its loads but the records are independent: the outputs, 32 pieces at
+// a time, and the maxima and sums (a thread per piece) for their weights.
+constexpr int kFewThreads = 512;
+template <typename T, int D>
+__global__ void __launch_bounds__(kFewThreads)
+paged_attn_join_few_kernel(const __grid_constant__ Params p, int ctas) {
+  constexpr int LPR = 16;                          // threads across the columns
+  constexpr int NP = kFewThreads / LPR;            // pieces in flight
+  constexpr int WARPS = kFewThreads / 32;
+  static_assert(kMaxCtas <= kFewThreads, "a thread per CTA");
+  __shared__ float sw[kMaxCtas], so[NP][64], red[2][WARPS];
+  __shared__ int found[WARPS + 1];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int valid = tid < ctas ? p.rec[tid].valid : 0;
+  const uint32_t mask = __ballot_sync(0xffffffffu, valid != 0);
+  if (lane == 0) found[warp] = __popc(mask);
+  if (tid == 0) found[WARPS] = -1;
+  __syncthreads();
+  int nth = __popc(mask & ((1u << lane) - 1));
+#pragma unroll 1
+  for (int i = 0; i < warp; ++i) nth += found[i];
+  if (valid != 0 && nth == (int)blockIdx.x) found[WARPS] = tid;
+  __syncthreads();
+  const int c0 = found[WARPS];
+  if (c0 < 0) return;
+  const SplitRec r = p.rec[c0];
+  const int row = blockIdx.y, x = r.x0 + row / 8, t = p.by_NG.quot(x), h = (x - t * p.NG) * 8 + row % 8;
+  if (row >= r.nvalid * 8 || h >= p.G) return;
+  const int k = tid / LPR, col = (tid % LPR) * 4, e = blockIdx.z * 64 + col, n = r.pieces;
+  float v[4][4];
+#pragma unroll
+  for (int u = 0; u < 4; ++u)
+    if (k + u * NP < n) load4(p.part_o + piece_row(c0, k + u * NP, gridDim.y, row) * D + e, v[u]);
+  const float2 ml = tid < n ? *reinterpret_cast<const float2*>(p.part_ml + piece_row(c0, tid, gridDim.y, row) * 2)
+                            : make_float2(-INFINITY, 0.f);
+  float gt[4];
+  if (k == 0) gate4<T>(p.a, r.bos + t, r.kvh * p.G + h, e, gt);
+  float m = ml.x;
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
   if (lane == 0) red[0][warp] = m;
   __syncthreads();
 #pragma unroll
-  for (int i = 0; i < kJoinThreads / 32; ++i) m = fmaxf(m, red[0][i]);
-  float l = 0.f;
-#pragma unroll
-  for (int i = 0; i < kMaxCtas / kJoinThreads; ++i) {
-    const float w = exp2f(ml[i].x - (m == -INFINITY ? 0.f : m));
-    l = fmaf(w, ml[i].y, l);
-    sw[tid + i * kJoinThreads] = w;
-  }
+  for (int i = 0; i < WARPS; ++i) m = fmaxf(m, red[0][i]);
+  const float w = ex2(ml.x - (m == -INFINITY ? 0.f : m));
+  float l = w * ml.y;
+  sw[tid] = w;
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
   if (lane == 0) red[1][warp] = l;
   __syncthreads();
   l = 0.f;
 #pragma unroll
-  for (int i = 0; i < kJoinThreads / 32; ++i) l += red[1][i];
-  const int k = tid / LPR, e = (tid % LPR) * 4;
+  for (int i = 0; i < WARPS; ++i) l += red[1][i];
   float y[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
-  for (int i = k; i < n; i += NP) {
-    float v[4];
-    load4(p.part_o + at(i) * D + e, v);
-    const float f = sw[i];
+#pragma unroll 1
+  for (int i = k; i < n; i += 4 * NP) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) y[j] = fmaf(v[j], f, y[j]);
+    for (int u = 0; u < 4; ++u) {
+      if (i + u * NP >= n) break;
+      const float f = sw[i + u * NP];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) y[j] = fmaf(v[u][j], f, y[j]);
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int next = i + (4 + u) * NP;
+      if (next < n) load4(p.part_o + piece_row(c0, next, gridDim.y, row) * D + e, v[u]);
+    }
   }
-  store4(&so[k][e], y);
+  store4(&so[k][col], y);
   __syncthreads();
   if (k != 0) return;
-  const float inv = l == 0.f ? 0.f : 1.f / l;
+  const float inv = l == 0.f ? 0.f : rcp(l);
 #pragma unroll
   for (int i = 1; i < NP; ++i)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) y[j] += so[i][e + j];
+    for (int j = 0; j < 4; ++j) y[j] += so[i][col + j];
 #pragma unroll
   for (int j = 0; j < 4; ++j) y[j] *= inv;
-  finish4<T>(p.a, r.bos + x / p.NG, r.kvh * p.G + h, e, D, y);
+  finish4(p.a, r.bos + t, r.kvh * p.G + h, e, D, gt, y);
 }
 
 // ------------------------------------------------------------------ host
@@ -976,6 +1136,8 @@ cudaError_t launch_c(const PagedAttnArgs& a, cudaStream_t s) {
   p.a = a;
   p.G = a.Nq / a.Nkv;
   p.NG = (p.G + 7) / 8;
+  p.by_NG = Div::of(p.NG);
+  p.by_page = Div::of(a.c.page_size);
   p.box = std::gcd(a.c.page_size, C::TILE);
   p.align = ((int64_t)a.c.max_pages * a.c.page_size + C::TILE - 1) / C::TILE <= kAlignTiles;
   p.c = a.scale * kLog2e;
@@ -991,16 +1153,20 @@ cudaError_t launch_c(const PagedAttnArgs& a, cudaStream_t s) {
   fn<<<grid, C::THREADS, C::SMEM, s>>>(mk, mv, p);
   e = cudaGetLastError();
   if (e != cudaSuccess || p.align) return e;
+  // at most so many units can be cut: few units have many pieces each
+  const int64_t units = (int64_t)a.Nkv * (a.num_seqs + (int64_t)a.total * p.NG / NT);
+  const bool few = units <= grid / 8;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(grid, C::ROWS);
-  cfg.blockDim = dim3(kJoinThreads);
+  cfg.gridDim = few ? dim3((int)units, C::ROWS, D / 64) : dim3(grid, std::max(1, NT * D / 256));
+  cfg.blockDim = dim3(few ? kFewThreads : kJoinThreads);
   cfg.stream = s;
   cudaLaunchAttribute at{};
   at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, paged_attn_join_kernel<T, D>, p);
+  return few ? cudaLaunchKernelEx(&cfg, paged_attn_join_few_kernel<T, D>, p, grid)
+             : cudaLaunchKernelEx(&cfg, paged_attn_join_kernel<T, D>, p, (int)C::ROWS);
 }
 
 template <int D>
