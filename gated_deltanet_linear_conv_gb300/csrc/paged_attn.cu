@@ -902,109 +902,181 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
       }
       break;
     }
-    // four columns per thread at a time, the next ones' gates loaded ahead
-    const int groups4 = d.nvalid * 8 * (D / 4);
-    auto place = [&](int i, int& tok) {            // head of group i (-1: no such row), and token
-      const int r = i / (D / 4), x = d.x0 + r / 8, t = p.by_NG.quot(x), h = (x - t * p.NG) * 8 + r % 8;
-      tok = d.bos + t;
-      return i < groups4 && h < p.G ? d.kvh * p.G + h : -1;
-    };
-    int tok, hd = place(tid, tok);
-    float gt[4];
-    if (hd >= 0 && d.slot < 0) gate4<T>(a, tok, hd, tid % (D / 4) * 4, gt);
-#pragma unroll 1
-    for (int i = tid; i < groups4; i += C::CW * 32) {
-      const int r = i / (D / 4), e = (i % (D / 4)) * 4;
-      int ntok, nhd = place(i + C::CW * 32, ntok);
-      float ngt[4];
-      if (nhd >= 0 && d.slot < 0) gate4<T>(a, ntok, nhd, (i + C::CW * 32) % (D / 4) * 4, ngt);
-      if (hd >= 0) {
-        float mt = -INFINITY, lt = 0.f, y[4] = {0.f, 0.f, 0.f, 0.f};
+    // a thread per row: each share's weight in the row (in place of its maximum)
+    if (tid < d.nvalid * 8) {
+      float mt = -INFINITY, lt = 0.f, f[C::TG];
 #pragma unroll
-        for (int k = 0; k < C::TG; ++k) mt = fmaxf(mt, jm[k * C::ROWS + r]);
+      for (int k = 0; k < C::TG; ++k) mt = fmaxf(mt, jm[k * C::ROWS + tid]);
+      const float base = mt == -INFINITY ? 0.f : mt;
 #pragma unroll
-        for (int k = 0; k < C::TG; ++k) {
-          const float mk_ = jm[k * C::ROWS + r];
-          if (mk_ == -INFINITY) continue;          // nothing in there (a row without slices is not written)
-          const float f = ex2(mk_ - mt);
-          const float4 v = *reinterpret_cast<const float4*>(jo + (k * C::ROWS + r) * C::JP + e);
-          lt = fmaf(jl[k * C::ROWS + r], f, lt);
-          y[0] = fmaf(v.x, f, y[0]); y[1] = fmaf(v.y, f, y[1]);
-          y[2] = fmaf(v.z, f, y[2]); y[3] = fmaf(v.w, f, y[3]);
-        }
-        if (d.slot < 0) {
-          const float inv = lt == 0.f ? 0.f : rcp(lt);
-#pragma unroll
-          for (int k = 0; k < 4; ++k) y[k] *= inv;
-          finish4(a, tok, hd, e, D, gt, y);
-        } else {
-          const int64_t at = (int64_t)d.slot * C::ROWS + r;
-          store4(p.part_o + at * D + e, y);
-          if (e == 0) *reinterpret_cast<float2*>(p.part_ml + at * 2) = make_float2(mt, lt);
-        }
+      for (int k = 0; k < C::TG; ++k) {
+        f[k] = ex2(jm[k * C::ROWS + tid] - base);
+        lt = fmaf(jl[k * C::ROWS + tid], f[k], lt);
       }
-      tok = ntok;
-      hd = nhd;
+      const float inv = d.slot >= 0 ? 1.f : lt == 0.f ? 0.f : rcp(lt);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) gt[k] = ngt[k];
+      for (int k = 0; k < C::TG; ++k) jm[k * C::ROWS + tid] = f[k] * inv;
+      if (d.slot >= 0)
+        *reinterpret_cast<float2*>(p.part_ml + ((int64_t)d.slot * C::ROWS + tid) * 2) = make_float2(mt, lt);
+    }
+    tc::named_sync(1, C::CW * 32);
+    auto joined = [&](int r, int e, float (&y)[4]) {
+      y[0] = y[1] = y[2] = y[3] = 0.f;
+#pragma unroll
+      for (int k = 0; k < C::TG; ++k) {
+        const float f = jm[k * C::ROWS + r];
+        if (f == 0.f) continue;                    // (the outputs of a share without slices are not written)
+        const float4 v = *reinterpret_cast<const float4*>(jo + (k * C::ROWS + r) * C::JP + e);
+        y[0] = fmaf(v.x, f, y[0]); y[1] = fmaf(v.y, f, y[1]);
+        y[2] = fmaf(v.z, f, y[2]); y[3] = fmaf(v.w, f, y[3]);
+      }
+    };
+    const int groups4 = d.nvalid * 8 * (D / 4);
+    if (d.slot >= 0) {
+      float* po = p.part_o + (int64_t)d.slot * C::ROWS * D;
+#pragma unroll 4
+      for (int i = tid; i < groups4; i += C::CW * 32) {
+        float y[4];
+        joined(i / (D / 4), i % (D / 4) * 4, y);
+        store4(po + i * 4, y);
+      }
+    } else {
+      // the next four columns' gate loaded ahead
+      auto place = [&](int i, int& tok) {          // head of group i (-1: no such row), and token
+        const int r = i / (D / 4), x = d.x0 + r / 8, t = p.by_NG.quot(x), h = (x - t * p.NG) * 8 + r % 8;
+        tok = d.bos + t;
+        return i < groups4 && h < p.G ? d.kvh * p.G + h : -1;
+      };
+      int tok, hd = place(tid, tok);
+      float gt[4];
+      if (hd >= 0) gate4<T>(a, tok, hd, tid % (D / 4) * 4, gt);
+#pragma unroll 1
+      for (int i = tid; i < groups4; i += C::CW * 32) {
+        int ntok, nhd = place(i + C::CW * 32, ntok);
+        float ngt[4];
+        if (nhd >= 0) gate4<T>(a, ntok, nhd, (i + C::CW * 32) % (D / 4) * 4, ngt);
+        if (hd >= 0) {
+          float y[4];
+          joined(i / (D / 4), i % (D / 4) * 4, y);
+          finish4(a, tok, hd, i % (D / 4) * 4, D, gt, y);
+        }
+        tok = ntok;
+        hd = nhd;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) gt[k] = ngt[k];
+      }
     }
     tc::named_sync(1, C::CW * 32);
   }
 }
 
 // ------------------------------------------------------------------ the join
-// Launched while the main kernel runs; the first step is to wait for its end.  Two forms,
-// so that neither many cut units start blocks for nothing nor a long one is joined by few.
+// Launched while the main kernel runs; the first step is to wait for its end.  Three forms,
+// by how many units can be cut at most, so that neither blocks start for nothing nor many
+// pieces wait for one another.
 //
-// Many units (so few pieces each): block (c, y) joins the unit that starts in CTA c's range
-// and ends behind it, if there is one; a thread takes four columns of a row, piece by piece.
+// PG = 1, about as many units as CTAs (about two pieces each): blocks (c, y) join the unit that starts
+// in CTA c's range and ends behind it, if there is one; a thread takes four columns of a row.
+// PG = 4, fewer units: blocks (u, y) join the unit of the u-th CTA with a record; four lanes
+// share four columns, each with every fourth piece.
 constexpr int kJoinThreads = 256;
 __device__ __forceinline__ int64_t piece_row(int c0, int i, int rows, int row) {
   // CTA c0's last piece (slot 2 c0 + 1), then the first ones of the CTAs behind it
   return ((int64_t)2 * (c0 + i) + (i == 0 ? 1 : 0)) * rows + row;
 }
-template <typename T, int D>
+// The nth CTA with a record, -1 if there are fewer (all threads of the block; PER * threads >= CTAs).
+template <int THREADS>
+__device__ __forceinline__ int nth_record(const Params& p, int ctas, int nth, int* found) {
+  constexpr int PER = (kMaxCtas + THREADS - 1) / THREADS, WARPS = THREADS / 32;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  int valid[PER], cnt = 0;
+  uint32_t mask[PER];
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const int c = (warp * PER + i) * 32 + lane;
+    valid[i] = c < ctas ? p.rec[c].valid : 0;
+  }
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    mask[i] = __ballot_sync(0xffffffffu, valid[i] != 0);
+    cnt += __popc(mask[i]);
+  }
+  if (lane == 0) found[warp] = cnt;
+  if (tid == 0) found[WARPS] = -1;
+  __syncthreads();
+  int at = 0;
+#pragma unroll
+  for (int i = 0; i < WARPS; ++i) at += i < warp ? found[i] : 0;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    if (valid[i] != 0 && at + __popc(mask[i] & ((1u << lane) - 1)) == nth) found[WARPS] = (warp * PER + i) * 32 + lane;
+    at += __popc(mask[i]);
+  }
+  __syncthreads();
+  return found[WARPS];
+}
+template <typename T, int D, int PG>
 __global__ void __launch_bounds__(kJoinThreads)
-paged_attn_join_kernel(const __grid_constant__ Params p, int rows) {
+paged_attn_join_kernel(const __grid_constant__ Params p, int ctas, int rows) {
+  __shared__ int found[kJoinThreads / 32 + 1];
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const SplitRec r = p.rec[blockIdx.x];
-  if (!r.valid) return;
+  int c0 = blockIdx.x;
+  if (PG > 1) {
+    c0 = nth_record<kJoinThreads>(p, ctas, blockIdx.x, found);
+    if (c0 < 0) return;
+  }
+  const SplitRec r = p.rec[c0];
+  // lanes: 32 / PG column groups side by side, PG times
+  const int lane = threadIdx.x & 31, k0 = lane / (32 / PG);
+  const int i = (blockIdx.y * (kJoinThreads / 32) + (threadIdx.x >> 5)) * (32 / PG) + lane % (32 / PG);
+  const int row = i / (D / 4), e = (i % (D / 4)) * 4;
+  const int x = r.x0 + row / 8, t = p.by_NG.quot(x), h = (x - t * p.NG) * 8 + row % 8;
+  const bool live = r.valid && row < r.nvalid * 8 && h < p.G;
+  if (!__any_sync(0xffffffffu, live)) return;
+  float gt[4], m = -INFINITY, l = 0.f, y[4] = {0.f, 0.f, 0.f, 0.f};
+  if (live && k0 == 0) gate4<T>(p.a, r.bos + t, r.kvh * p.G + h, e, gt);
 #pragma unroll 1
-  for (int i = blockIdx.y * kJoinThreads + threadIdx.x; i < r.nvalid * 8 * (D / 4); i += gridDim.y * kJoinThreads) {
-    const int row = i / (D / 4), e = (i % (D / 4)) * 4;
-    const int x = r.x0 + row / 8, t = p.by_NG.quot(x), h = (x - t * p.NG) * 8 + row % 8;
-    if (h >= p.G) continue;
-    float gt[4], m = -INFINITY, l = 0.f, y[4] = {0.f, 0.f, 0.f, 0.f};
-    gate4<T>(p.a, r.bos + t, r.kvh * p.G + h, e, gt);
-#pragma unroll 1
-    for (int j0 = 0; j0 < r.pieces; j0 += 4) {
-      float2 ml[4];
-      float v[4][4];
+  for (int j0 = k0; live && j0 < r.pieces; j0 += 4 * PG) {
+    float2 ml[4];
+    float v[4][4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        ml[j] = make_float2(-INFINITY, 0.f);
-        if (j0 + j < r.pieces) {
-          const int64_t at = piece_row(blockIdx.x, j0 + j, rows, row);
-          ml[j] = *reinterpret_cast<const float2*>(p.part_ml + at * 2);
-          load4(p.part_o + at * D + e, v[j]);
-        }
-      }
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        if (j0 + j >= r.pieces) break;
-        const float mn = fmaxf(m, ml[j].x), base = mn == -INFINITY ? 0.f : mn;
-        const float f0 = ex2(m - base), f1 = ex2(ml[j].x - base);
-        l = l * f0 + ml[j].y * f1;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) y[k] = y[k] * f0 + v[j][k] * f1;
-        m = mn;
+    for (int j = 0; j < 4; ++j) {
+      ml[j] = make_float2(-INFINITY, 0.f);
+      v[j][0] = v[j][1] = v[j][2] = v[j][3] = 0.f;
+      if (j0 + j * PG < r.pieces) {
+        const int64_t at = piece_row(c0, j0 + j * PG, rows, row);
+        ml[j] = *reinterpret_cast<const float2*>(p.part_ml + at * 2);
+        load4(p.part_o + at * D + e, v[j]);
       }
     }
-    const float inv = l == 0.f ? 0.f : rcp(l);
+    const float mn = fmaxf(fmaxf(fmaxf(m, ml[0].x), fmaxf(ml[1].x, ml[2].x)), ml[3].x);
+    const float base = mn == -INFINITY ? 0.f : mn, f0 = ex2(m - base);
+    l *= f0;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) y[k] *= inv;
-    finish4(p.a, r.bos + t, r.kvh * p.G + h, e, D, gt, y);
+    for (int k = 0; k < 4; ++k) y[k] *= f0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float f = ex2(ml[j].x - base);
+      l = fmaf(ml[j].y, f, l);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) y[k] = fmaf(v[j][k], f, y[k]);
+    }
+    m = mn;
   }
+#pragma unroll
+  for (int off = 32 / PG; off < 32; off <<= 1) {   // the lanes that share the columns
+    const float mo = __shfl_xor_sync(0xffffffffu, m, off), mn = fmaxf(m, mo), base = mn == -INFINITY ? 0.f : mn;
+    const float f0 = ex2(m - base), f1 = ex2(mo - base);
+    l = l * f0 + __shfl_xor_sync(0xffffffffu, l, off) * f1;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) y[k] = y[k] * f0 + __shfl_xor_sync(0xffffffffu, y[k], off) * f1;
+    m = mn;
+  }
+  if (!live || k0 != 0) return;
+  const float inv = l == 0.f ? 0.f : rcp(l);
+#pragma unroll
+  for (int k = 0; k < 4; ++k) y[k] *= inv;
+  finish4(p.a, r.bos + t, r.kvh * p.G + h, e, D, gt, y);
 }
 
 // Few units (so many pieces): block (u, row, z) joins 64 columns of a row of the u-th CTA
@@ -1018,29 +1090,20 @@ paged_attn_join_few_kernel(const __grid_constant__ Params p, int ctas) {
   constexpr int NP = kFewThreads / LPR;            // pieces in flight
   constexpr int WARPS = kFewThreads / 32;
   static_assert(kMaxCtas <= kFewThreads, "a thread per CTA");
-  __shared__ float sw[kMaxCtas], so[NP][64], red[2][WARPS];
+  __shared__ float sw[kMaxCtas], so[WARPS][64], red[2][WARPS];
   __shared__ int found[WARPS + 1];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int valid = tid < ctas ? p.rec[tid].valid : 0;
-  const uint32_t mask = __ballot_sync(0xffffffffu, valid != 0);
-  if (lane == 0) found[warp] = __popc(mask);
-  if (tid == 0) found[WARPS] = -1;
-  __syncthreads();
-  int nth = __popc(mask & ((1u << lane) - 1));
-#pragma unroll 1
-  for (int i = 0; i < warp; ++i) nth += found[i];
-  if (valid != 0 && nth == (int)blockIdx.x) found[WARPS] = tid;
-  __syncthreads();
-  const int c0 = found[WARPS];
+  const int c0 = nth_record<kFewThreads>(p, ctas, blockIdx.x, found);
   if (c0 < 0) return;
   const SplitRec r = p.rec[c0];
   const int row = blockIdx.y, x = r.x0 + row / 8, t = p.by_NG.quot(x), h = (x - t * p.NG) * 8 + row % 8;
   if (row >= r.nvalid * 8 || h >= p.G) return;
+  constexpr int U = 5;                             // (two units over 304 CTAs: all of their 152 pieces at once)
   const int k = tid / LPR, col = (tid % LPR) * 4, e = blockIdx.z * 64 + col, n = r.pieces;
-  float v[4][4];
+  float v[U][4];
 #pragma unroll
-  for (int u = 0; u < 4; ++u)
+  for (int u = 0; u < U; ++u)
     if (k + u * NP < n) load4(p.part_o + piece_row(c0, k + u * NP, gridDim.y, row) * D + e, v[u]);
   const float2 ml = tid < n ? *reinterpret_cast<const float2*>(p.part_ml + piece_row(c0, tid, gridDim.y, row) * 2)
                             : make_float2(-INFINITY, 0.f);
@@ -1065,28 +1128,33 @@ paged_attn_join_few_kernel(const __grid_constant__ Params p, int ctas) {
   for (int i = 0; i < WARPS; ++i) l += red[1][i];
   float y[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 1
-  for (int i = k; i < n; i += 4 * NP) {
+  for (int i = k; i < n; i += U * NP) {
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
+    for (int u = 0; u < U; ++u) {
       if (i + u * NP >= n) break;
       const float f = sw[i + u * NP];
 #pragma unroll
       for (int j = 0; j < 4; ++j) y[j] = fmaf(v[u][j], f, y[j]);
     }
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const int next = i + (4 + u) * NP;
+    for (int u = 0; u < U; ++u) {
+      const int next = i + (U + u) * NP;
       if (next < n) load4(p.part_o + piece_row(c0, next, gridDim.y, row) * D + e, v[u]);
     }
   }
-  store4(&so[k][col], y);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) y[j] += __shfl_xor_sync(0xffffffffu, y[j], LPR);
+  if (lane < LPR) store4(&so[warp][col], y);
   __syncthreads();
   if (k != 0) return;
   const float inv = l == 0.f ? 0.f : rcp(l);
 #pragma unroll
-  for (int i = 1; i < NP; ++i)
+  for (int i = 1; i < WARPS; ++i) {
+    float o[4];
+    load4(&so[i][col], o);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) y[j] += so[i][col + j];
+    for (int j = 0; j < 4; ++j) y[j] += o[j];
+  }
 #pragma unroll
   for (int j = 0; j < 4; ++j) y[j] *= inv;
   finish4(p.a, r.bos + t, r.kvh * p.G + h, e, D, gt, y);
@@ -1153,11 +1221,16 @@ cudaError_t launch_c(const PagedAttnArgs& a, cudaStream_t s) {
   fn<<<grid, C::THREADS, C::SMEM, s>>>(mk, mv, p);
   e = cudaGetLastError();
   if (e != cudaSuccess || p.align) return e;
-  // at most so many units can be cut: few units have many pieces each
-  const int64_t units = (int64_t)a.Nkv * (a.num_seqs + (int64_t)a.total * p.NG / NT);
-  const bool few = units <= grid / 8;
+  // at most so many units can be cut, into so many pieces each on average
+  const int64_t per_seq = a.cu == nullptr ? ((int64_t)(a.total / a.num_seqs) * p.NG + NT - 1) / NT : 0;
+  const int64_t units = a.cu == nullptr ? per_seq * a.num_seqs * a.Nkv
+                                        : (int64_t)a.Nkv * (a.num_seqs + (int64_t)a.total * p.NG / NT);
+  const bool few = units * 16 <= grid && units * C::ROWS * (D / 64) <= 4 * num_sms();
+  const bool many = units * 2 > grid;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = few ? dim3((int)units, C::ROWS, D / 64) : dim3(grid, std::max(1, NT * D / 256));
+  cfg.gridDim = few ? dim3((int)units, C::ROWS, D / 64)
+                    : many ? dim3(grid, (C::ROWS * D / 4 + kJoinThreads - 1) / kJoinThreads)
+                           : dim3((int)units, C::ROWS * D / kJoinThreads);
   cfg.blockDim = dim3(few ? kFewThreads : kJoinThreads);
   cfg.stream = s;
   cudaLaunchAttribute at{};
@@ -1165,8 +1238,9 @@ cudaError_t launch_c(const PagedAttnArgs& a, cudaStream_t s) {
   at.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &at;
   cfg.numAttrs = 1;
-  return few ? cudaLaunchKernelEx(&cfg, paged_attn_join_few_kernel<T, D>, p, grid)
-             : cudaLaunchKernelEx(&cfg, paged_attn_join_kernel<T, D>, p, (int)C::ROWS);
+  if (few) return cudaLaunchKernelEx(&cfg, paged_attn_join_few_kernel<T, D>, p, grid);
+  return many ? cudaLaunchKernelEx(&cfg, paged_attn_join_kernel<T, D, 1>, p, grid, (int)C::ROWS)
+              : cudaLaunchKernelEx(&cfg, paged_attn_join_kernel<T, D, 4>, p, grid, (int)C::ROWS);
 }
 
 template <int D>
