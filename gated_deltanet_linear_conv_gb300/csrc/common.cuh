@@ -166,4 +166,9 @@ __device__ __forceinline__ void check_seqs(const int32_t* cu, int num_seqs, int 
   }
 }
 
+// Programmatic launches: until the kernels before this one have ended and their writes are
+// visible; and leave for the next kernel to be set up (it waits in turn).
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void pdl_launch_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 }  // namespace gdn

@@ -145,4 +145,22 @@ struct PagedAttnArgs {
 size_t paged_attn_workspace_bytes(int num_seqs, int total, int Nq, int Nkv, int D);
 cudaError_t launch_paged_attn(const PagedAttnArgs& p, cudaStream_t s);
 
+// Launch that may begin while the kernel before it on the stream still runs: the kernel has to
+// wait (pdl_wait) in every thread before it touches global memory, so that its end implies the
+// end of all that was launched before it.  Its start-up overlaps the other's end.
+template <typename... P, typename... A>
+inline cudaError_t launch_early(void (*fn)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t s, A&&... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, fn, static_cast<P>(args)...);
+}
+
 }  // namespace gdn

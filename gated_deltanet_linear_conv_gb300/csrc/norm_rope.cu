@@ -58,6 +58,8 @@ norm_rope_kernel(const __grid_constant__ NormRopeArgs p) {
   const bool live = t < p.total;
   const int lane = threadIdx.x & 31;
 
+  pdl_launch_next();
+  pdl_wait();
   Chunk<Tin> raw[kRows];
 #pragma unroll
   for (int u = 0; u < kRows; ++u) {
@@ -178,9 +180,8 @@ cudaError_t launch_d(const NormRopeArgs& p, cudaStream_t s) {
   if (p.total == 0 || rows == 0) return cudaSuccess;
   const int per_block = kThreads / (D / 8);
   const dim3 grid((p.total + per_block - 1) / per_block, (rows + kRows - 1) / kRows);
-  if (cache) norm_rope_kernel<Tin, Tq, Tkv, D, true><<<grid, kThreads, 0, s>>>(p);
-  else norm_rope_kernel<Tin, Tq, Tkv, D, false><<<grid, kThreads, 0, s>>>(p);
-  return cudaGetLastError();
+  return cache ? launch_early(norm_rope_kernel<Tin, Tq, Tkv, D, true>, grid, dim3(kThreads), 0, s, p)
+               : launch_early(norm_rope_kernel<Tin, Tq, Tkv, D, false>, grid, dim3(kThreads), 0, s, p);
 }
 
 template <typename Tin, typename Tq, typename Tkv>

@@ -645,7 +645,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
   const PagedAttnArgs& a = p.a;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  pdl_launch_next();
   if (tid == C::CW * 32) {
 #pragma unroll 1
     for (int i = 0; i < C::STAGES; ++i) {
@@ -659,6 +659,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
     tc::prefetch_tmap(&mk);
     tc::prefetch_tmap(&mv);
   }
+  pdl_wait();
   // all tiles, and the sequence that this CTA's range starts in
   const int per = (a.num_seqs + C::THREADS - 1) / C::THREADS;
   const int s_lo = min(a.num_seqs, tid * per), s_hi = min(a.num_seqs, s_lo + per);
@@ -1019,7 +1020,8 @@ template <typename T, int D, int PG>
 __global__ void __launch_bounds__(kJoinThreads)
 paged_attn_join_kernel(const __grid_constant__ Params p, int ctas, int rows) {
   __shared__ int found[kJoinThreads / 32 + 1];
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  pdl_launch_next();
+  pdl_wait();
   int c0 = blockIdx.x;
   if (PG > 1) {
     c0 = nth_record<kJoinThreads>(p, ctas, blockIdx.x, found);
@@ -1093,7 +1095,8 @@ paged_attn_join_few_kernel(const __grid_constant__ Params p, int ctas) {
   __shared__ float sw[kMaxCtas], so[WARPS][64], red[2][WARPS];
   __shared__ int found[WARPS + 1];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  pdl_launch_next();
+  pdl_wait();
   const int c0 = nth_record<kFewThreads>(p, ctas, blockIdx.x, found);
   if (c0 < 0) return;
   const SplitRec r = p.rec[c0];
@@ -1218,8 +1221,7 @@ cudaError_t launch_c(const PagedAttnArgs& a, cudaStream_t s) {
   CUtensorMap mk, mv;
   const int cols = C::BF ? 64 : D;
   if (!cache_map(&mk, a.c.k, a, cols, p.box) || !cache_map(&mv, a.c.v, a, cols, p.box)) return cudaErrorInvalidValue;
-  fn<<<grid, C::THREADS, C::SMEM, s>>>(mk, mv, p);
-  e = cudaGetLastError();
+  e = launch_early(fn, dim3(grid), dim3(C::THREADS), C::SMEM, s, mk, mv, p);
   if (e != cudaSuccess || p.align) return e;
   // at most so many units can be cut, into so many pieces each on average
   const int64_t per_seq = a.cu == nullptr ? ((int64_t)(a.total / a.num_seqs) * p.NG + NT - 1) / NT : 0;
@@ -1227,20 +1229,14 @@ cudaError_t launch_c(const PagedAttnArgs& a, cudaStream_t s) {
                                         : (int64_t)a.Nkv * (a.num_seqs + (int64_t)a.total * p.NG / NT);
   const bool few = units * 16 <= grid && units * C::ROWS * (D / 64) <= 4 * num_sms();
   const bool many = units * 2 > grid;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = few ? dim3((int)units, C::ROWS, D / 64)
-                    : many ? dim3(grid, (C::ROWS * D / 4 + kJoinThreads - 1) / kJoinThreads)
-                           : dim3((int)units, C::ROWS * D / kJoinThreads);
-  cfg.blockDim = dim3(few ? kFewThreads : kJoinThreads);
-  cfg.stream = s;
-  cudaLaunchAttribute at{};
-  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &at;
-  cfg.numAttrs = 1;
-  if (few) return cudaLaunchKernelEx(&cfg, paged_attn_join_few_kernel<T, D>, p, grid);
-  return many ? cudaLaunchKernelEx(&cfg, paged_attn_join_kernel<T, D, 1>, p, grid, (int)C::ROWS)
-              : cudaLaunchKernelEx(&cfg, paged_attn_join_kernel<T, D, 4>, p, grid, (int)C::ROWS);
+  if (few)
+    return launch_early(paged_attn_join_few_kernel<T, D>, dim3((int)units, C::ROWS, D / 64), dim3(kFewThreads), 0, s, p,
+                        grid);
+  if (many)
+    return launch_early(paged_attn_join_kernel<T, D, 1>, dim3(grid, (C::ROWS * D / 4 + kJoinThreads - 1) / kJoinThreads),
+                        dim3(kJoinThreads), 0, s, p, grid, (int)C::ROWS);
+  return launch_early(paged_attn_join_kernel<T, D, 4>, dim3((int)units, C::ROWS * D / kJoinThreads), dim3(kJoinThreads), 0,
+                      s, p, grid, (int)C::ROWS);
 }
 
 template <int D>
