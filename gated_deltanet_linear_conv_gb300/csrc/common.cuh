@@ -171,4 +171,16 @@ __device__ __forceinline__ void check_seqs(const int32_t* cu, int num_seqs, int 
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void pdl_launch_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
+// x / d for 0 <= x < 2^31 by one multiplication (d > 0): with 2^k the first power of two that is
+// at least d and m = floor(2^32 (2^k - d) / d) + 1, x / d = (hi32(x m) + x) >> k.
+struct Div {
+  uint32_t d, m, k;
+  static Div of(uint32_t d) {
+    uint32_t k = 0;
+    while ((uint64_t)1 << k < d) ++k;
+    return {d, (uint32_t)(((((uint64_t)1 << k) - d) << 32) / d + 1), k};
+  }
+  __device__ __forceinline__ int quot(int x) const { return (int)((__umulhi((uint32_t)x, m) + (uint32_t)x) >> k); }
+};
+
 }  // namespace gdn

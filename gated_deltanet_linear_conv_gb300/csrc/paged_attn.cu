@@ -116,18 +116,6 @@ struct Ranges {
   }
 };
 
-// x / d for 0 <= x < 2^31 by one multiplication (d > 0): with 2^k the first power of two that is
-// at least d and m = floor(2^32 (2^k - d) / d) + 1, x / d = (hi32(x m) + x) >> k.
-struct Div {
-  uint32_t d, m, k;
-  static Div of(uint32_t d) {
-    uint32_t k = 0;
-    while ((uint64_t)1 << k < d) ++k;
-    return {d, (uint32_t)(((((uint64_t)1 << k) - d) << 32) / d + 1), k};
-  }
-  __device__ __forceinline__ int quot(int x) const { return (int)((__umulhi((uint32_t)x, m) + (uint32_t)x) >> k); }
-};
-
 __host__ __device__ constexpr size_t align16(size_t x) { return (x + 15) & ~(size_t)15; }
 
 struct Params {
