@@ -11,8 +11,8 @@
 // kv head; all its columns see the same cache indices.  A unit is (sequence, kv head, NT
 // consecutive octets); its cache indices split into tiles of 8 KB of K and 8 KB of V.
 //
-// Work split.  All tiles of all units, laid end to end, are cut into one equal range per
-// CTA (two CTAs per SM, one's starts and joins under the other's stream), from kv_lens as
+// Work split.  All tiles of all units, laid end to end with a gap of kUnitCost for each
+// unit's start and join, are cut into one equal range per CTA (two CTAs per SM, one's starts and joins under the other's stream), from kv_lens as
 // they stand on the device: ragged batches and a single long context keep every SM equally
 // busy, and neither the host nor a captured graph needs the lengths.  A unit inside one
 // range is finished by its CTA; the pieces of a unit that crosses ranges (at most one cut
@@ -42,6 +42,7 @@ namespace {
 constexpr int kStageHalf = 8192;                   // bytes of K (and of V) in a stage
 constexpr int kAlignTiles = 16;                    // no unit longer than this: ranges end at unit borders
 constexpr int kMinTiles = 4;                       // tiles of a range at least (fewer CTAs for little work)
+constexpr int kUnitCost = 4;                       // a unit's start and join, in tiles, where ranges are cut
 constexpr int kOcc = 2;                            // CTAs per SM
 constexpr int kMaxCtas = 512;                      // CTAs, and so pieces of a unit, at most
 constexpr uint64_t kWaitNs = 2000000000ull;        // bound of every wait
@@ -49,11 +50,12 @@ constexpr uint32_t kPollCap = 1u << 28;
 constexpr float kLog2e = 1.4426950408889634f;
 
 // ------------------------------------------------------------------ shapes
-template <typename T, int D, int NT_>
+template <typename T, int D, int NT_, int RG_ = 8>
 struct Cfg {
   static constexpr bool BF = sizeof(T) == 2;
   static constexpr int NT = NT_;                                   // octets per pass
-  static constexpr int ROWS = NT * 8;
+  static constexpr int RG = RG_;                                   // rows of an octet: 8, or 4 where four heads are all
+  static constexpr int ROWS = NT * RG;
   static constexpr int CW = 4;                                     // consumer warps
   static constexpr int THREADS = (CW + 1) * 32;
   static constexpr int DS = BF && NT * D > 256 ? NT * D / 256 : 1; // warps that share a slice
@@ -120,7 +122,7 @@ __host__ __device__ constexpr size_t align16(size_t x) { return (x + 15) & ~(siz
 
 struct Params {
   PagedAttnArgs a;
-  int G, NG;               // query heads per kv head, octets per token
+  int G, NG, rg_log;           // query heads per kv head, octets per token, log2 of the rows of an octet
   Div by_NG, by_page;
   int box, align;          // slots per TMA box; ranges end at unit borders
   float c;                 // scale * log2(e)
@@ -225,7 +227,7 @@ __device__ __forceinline__ int seq_groups(const Params& p, const Seq& q) {   // 
 
 template <typename C>
 __device__ __forceinline__ int64_t seq_work(const Params& p, const Seq& q) {
-  return q.len == 0 ? 0 : (int64_t)seq_tiles<C>(q) * seq_groups<C>(p, q) * p.a.Nkv;
+  return q.len == 0 ? 0 : (int64_t)(seq_tiles<C>(q) + kUnitCost) * seq_groups<C>(p, q) * p.a.Nkv;
 }
 
 // The next sequence behind s with anything to attend (the warp looks at 32 at a time); its
@@ -323,6 +325,7 @@ struct TcWarp {
         for (int e = 0; e < 4; ++e) o[nt][i][e] = 0.f;
   }
 
+  static constexpr bool QREG = true;
   // Slice of the 16 tokens from tok0, rows j0.. of the stage; lim(nt): tokens octet nt sees.
   template <typename Lim>
   __device__ __forceinline__ void slice(uint8_t* ks_, uint8_t* vs_, int j0, int tok0, int nvalid, float c, Lim lim,
@@ -492,69 +495,86 @@ struct TcWarp {
   }
 };
 
-// float32 on the CUDA cores: the lanes of a warp span a head row, four tokens at a time.
-// The 8 x 4 partial dot products are summed over the lanes by folding halves onto each
-// other (9 exchanges per token), which leaves lane 4 h + i with the score of head h and
-// token i: one exponential per lane.
-template <int D>
+// float32 on the CUDA cores, four tokens at a time.  Eight lanes span a head row; the four
+// groups of eight take two heads each (or one, where the kv head has at most four), so that
+// a dot product is summed over 8 lanes only: with 32 lanes across the row the exchanges were
+// half of the instructions (147 per token and warp, 54 % of the issue slots).  The sums end
+// with one score of the 8 x 4 per lane: one exponential each.  Element pairs go through the
+// packed fp32x2 operations.
+template <int D, int RG>
 struct SimtWarp {
-  using C = Cfg<float, D, 1>;
-  static constexpr int E = D / 32;                 // elements per lane
-  static constexpr int V = E < 4 ? E : 4;          // per load
-  float q[8][E], o[8][E];
-  float m, l;                                      // of head lane / 4
+  using C = Cfg<float, D, 1, RG>;
+  static constexpr int E = D / 32;                 // 4-element chunks per lane: columns 32 i + 4 (lane % 8)
+  static constexpr int H = RG / 4;                 // heads per lane group
+  static constexpr bool QREG = H * E < 16;         // queries in registers; at 64 of them they stay in shared memory
+  float2 q[QREG ? H : 1][QREG ? E : 1][2], o[H][E][2];
+  uint32_t q_at;
+  float m, l;                                      // of head `mine`
 
-  // element i of a lane sits at column (i / V) * 32 V + lane V + i % V
-  static __device__ __forceinline__ void row(const uint8_t* base, int r, int lane, float (&x)[E]) {
-    const float* p = reinterpret_cast<const float*>(base) + r * D + lane * V;
-    if (V == 4) {
-#pragma unroll
-      for (int i = 0; i < E; i += 4) {
-        const float4 f = *reinterpret_cast<const float4*>(p + i * 32);
-        x[i] = f.x; x[i + 1] = f.y; x[i + 2] = f.z; x[i + 3] = f.w;
-      }
-    } else {
-      const float2 f = *reinterpret_cast<const float2*>(p);
-      x[0] = f.x; x[1] = f.y;
-    }
+  static __device__ __forceinline__ int mine(int lane) { return RG == 8 ? lane >> 2 : lane >> 3; }
+  // lane that holds the score of this lane group's head h, token i
+  static __device__ __forceinline__ int holder(int lane, int h, int i) { return (lane & 24) + h * 4 + i; }
+  static __device__ __forceinline__ void chunk(uint32_t at, float2 (&x)[2]) {
+    asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(x[0].x), "=f"(x[0].y), "=f"(x[1].x), "=f"(x[1].y)
+                 : "r"(at) : "memory");
   }
   __device__ __forceinline__ void start(const uint8_t* qs, int, uint8_t*, int lane) {
+    q_at = tc::smem_u32(qs) + (lane >> 3) * H * C::QPITCH + (lane & 7) * 16;
 #pragma unroll
-    for (int h = 0; h < 8; ++h) {
-      row(qs + h * C::QPITCH, 0, lane, q[h]);
+    for (int h = 0; h < H; ++h)
 #pragma unroll
-      for (int i = 0; i < E; ++i) o[h][i] = 0.f;
-    }
+      for (int e = 0; e < E; ++e) {
+        if (QREG) chunk(q_at + h * C::QPITCH + e * 128, q[h][e]);
+        o[h][e][0] = o[h][e][1] = make_float2(0.f, 0.f);
+      }
     m = -INFINITY;
     l = 0.f;
   }
   template <typename Lim>
-  __device__ __forceinline__ void slice(uint8_t* ks_, uint8_t* vs_, int j0, int tok0, int, float c, Lim lim, int,
-                                        int lane) {
+  __device__ __forceinline__ void slice(uint8_t* ks_, uint8_t* vs_, int j0, int tok0, int, float c, Lim lim,
+                                        int, int lane) {
     const int last = lim(0) - tok0;                // tokens of the slice that are visible (> 0)
+    const uint32_t k_at = tc::smem_u32(ks_) + j0 * (D * 4) + (lane & 7) * 16;
+    const uint32_t v_at = tc::smem_u32(vs_) + j0 * (D * 4) + (lane & 7) * 16;
+    float2 a[4][H];
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      float2 qe[H][2];
+#pragma unroll
+      for (int h = 0; h < H; ++h) {
+        if (QREG) {
+          qe[h][0] = q[h][e][0];
+          qe[h][1] = q[h][e][1];
+        } else {
+          chunk(q_at + h * C::QPITCH + e * 128, qe[h]);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float2 k[2];
+        chunk(k_at + i * (D * 4) + e * 128, k);
+#pragma unroll
+        for (int h = 0; h < H; ++h) {
+          a[i][h] = e == 0 ? __fmul2_rn(qe[h][0], k[0]) : __ffma2_rn(qe[h][0], k[0], a[i][h]);
+          a[i][h] = __ffma2_rn(qe[h][1], k[1], a[i][h]);
+        }
+      }
+    }
     float s = 0.f;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      float k[E], d[8];
-      row(ks_, j0 + i, lane, k);
-#pragma unroll
-      for (int h = 0; h < 8; ++h) {
-        d[h] = q[h][0] * k[0];
-#pragma unroll
-        for (int e = 1; e < E; ++e) d[h] = fmaf(q[h][e], k[e], d[h]);
+      float d;
+      if (H == 2) {                                // lanes 4..7 of a group go on with the second head
+        const bool up = (lane & 4) != 0;
+        const float d0 = a[i][0].x + a[i][0].y, d1 = a[i][H - 1].x + a[i][H - 1].y;
+        d = (up ? d1 : d0) + __shfl_xor_sync(0xffffffffu, up ? d0 : d1, 4);
+      } else {
+        d = a[i][0].x + a[i][0].y;
+        d += __shfl_xor_sync(0xffffffffu, d, 4);
       }
-#pragma unroll
-      for (int w = 4, off = 16; w >= 1; w >>= 1, off >>= 1) {
-        const bool up = (lane & off) != 0;
-#pragma unroll
-        for (int h = 0; h < w; ++h) {
-          const float keep = up ? d[h + w] : d[h], send = up ? d[h] : d[h + w];
-          d[h] = keep + __shfl_xor_sync(0xffffffffu, send, off);
-        }
-      }
-      d[0] += __shfl_xor_sync(0xffffffffu, d[0], 2);
-      d[0] += __shfl_xor_sync(0xffffffffu, d[0], 1);
-      if ((lane & 3) == i) s = d[0];
+      d += __shfl_xor_sync(0xffffffffu, d, 2);
+      d += __shfl_xor_sync(0xffffffffu, d, 1);
+      if ((lane & 3) == i) s = d;
     }
     s = (lane & 3) < last ? s * c : -INFINITY;
     float mx = fmaxf(s, __shfl_xor_sync(0xffffffffu, s, 1));
@@ -565,24 +585,32 @@ struct SimtWarp {
       m = mn;
       l *= al;
 #pragma unroll
-      for (int h = 0; h < 8; ++h) {
-        const float a = __shfl_sync(0xffffffffu, al, 4 * h);
+      for (int h = 0; h < H; ++h) {
+        const float a = __shfl_sync(0xffffffffu, al, holder(lane, h, 0));
 #pragma unroll
-        for (int e = 0; e < E; ++e) o[h][e] *= a;
+        for (int e = 0; e < E; ++e)
+#pragma unroll
+          for (int f = 0; f < 2; ++f) o[h][e][f] = __fmul2_rn(o[h][e][f], make_float2(a, a));
       }
     }
     const float p = ex2(s - (m == -INFINITY ? 0.f : m));
     l += p;
+    float w[4][H];                                 // 0 for rows that may hold anything: those are not read into o
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int h = 0; h < H; ++h) w[i][h] = __shfl_sync(0xffffffffu, p, holder(lane, h, i));
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      if (i < last) {                              // rows behind may hold anything: not read into o
-        float v[E];
-        row(vs_, j0 + i, lane, v);
+      if (i < last) {
 #pragma unroll
-        for (int h = 0; h < 8; ++h) {
-          const float w = __shfl_sync(0xffffffffu, p, 4 * h + i);
+        for (int e = 0; e < E; ++e) {
+          float2 v[2];
+          chunk(v_at + i * (D * 4) + e * 128, v);
 #pragma unroll
-          for (int e = 0; e < E; ++e) o[h][e] = fmaf(w, v[e], o[h][e]);
+          for (int h = 0; h < H; ++h)
+#pragma unroll
+            for (int f = 0; f < 2; ++f) o[h][e][f] = __ffma2_rn(make_float2(w[i][h], w[i][h]), v[f], o[h][e][f]);
         }
       }
     }
@@ -591,26 +619,28 @@ struct SimtWarp {
     float v = l;
     v += __shfl_xor_sync(0xffffffffu, v, 1);
     v += __shfl_xor_sync(0xffffffffu, v, 2);
-    if ((lane & 3) == 0) {
-      jm[lane >> 2] = m;
-      jl[lane >> 2] = v;
+    if ((lane & 3) == 0 && (RG == 8 || (lane & 4) == 0)) {
+      jm[mine(lane)] = m;
+      jl[mine(lane)] = v;
     }
     if (!any) return;
 #pragma unroll
-    for (int h = 0; h < 8; ++h)
+    for (int h = 0; h < H; ++h)
 #pragma unroll
-      for (int e = 0; e < E; ++e) jo[h * C::JP + (e / V) * 32 * V + lane * V + e % V] = o[h][e];
+      for (int e = 0; e < E; ++e)
+        *reinterpret_cast<float4*>(jo + ((lane >> 3) * H + h) * C::JP + e * 32 + (lane & 7) * 4) =
+            make_float4(o[h][e][0].x, o[h][e][0].y, o[h][e][1].x, o[h][e][1].y);
   }
 };
-template <typename T, int D, int NT> struct WarpOf { using type = TcWarp<D, NT>; };
-template <int D, int NT> struct WarpOf<float, D, NT> { using type = SimtWarp<D>; };
+template <typename T, int D, int NT, int RG> struct WarpOf { using type = TcWarp<D, NT>; };
+template <int D, int NT, int RG> struct WarpOf<float, D, NT, RG> { using type = SimtWarp<D, RG>; };
 
 // ------------------------------------------------------------------ the main kernel
-template <typename T, int D, int NT>
-__global__ void __launch_bounds__(Cfg<T, D, NT>::THREADS, kOcc)
+template <typename T, int D, int NT, int RG>
+__global__ void __launch_bounds__(Cfg<T, D, NT, RG>::THREADS, kOcc)
 paged_attn_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
                   const __grid_constant__ Params p) {
-  using C = Cfg<T, D, NT>;
+  using C = Cfg<T, D, NT, RG>;
   constexpr int COLS = 128 / (int)sizeof(T);       // columns of a box (128 bytes, swizzled) in bf16
   constexpr int CB = C::BF ? D / COLS : 1;         // boxes across a row; float32: whole rows, not swizzled
   extern __shared__ __align__(16) uint8_t raw[];
@@ -701,23 +731,27 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
       Seq q{from_seq[1], from_seq[2], from_seq[3]};
       int tiles = seq_tiles<C>(q), groups = seq_groups<C>(p, q);
       int64_t seq_at = *from, pos = lo;
-      int unit = div_small(pos - seq_at, tiles);
-      if (p.align && seq_at + (int64_t)unit * tiles < pos) ++unit;         // the first unit that starts here
-      if (p.align) pos = seq_at + (int64_t)unit * tiles;
+      int cost = tiles + kUnitCost;                // of a unit; its tiles lie at the end
+      int unit = div_small(pos - seq_at, cost);
+      if (p.align && seq_at + (int64_t)unit * cost < pos) ++unit;          // the first unit that starts here
+      if (p.align) pos = seq_at + (int64_t)unit * cost;
       const int nbox = C::TILE / p.box;
 #pragma unroll 1
       while (pos < hi) {
         if (unit >= groups * a.Nkv) {
-          seq_at += (int64_t)tiles * groups * a.Nkv;
+          seq_at += (int64_t)cost * groups * a.Nkv;
           s = next_seq(a, s, &q);
           if (s >= a.num_seqs) break;              // (cannot be: pos < hi <= total)
           tiles = seq_tiles<C>(q);
           groups = seq_groups<C>(p, q);
+          cost = tiles + kUnitCost;
           unit = 0;
           continue;
         }
-        const int t0 = (int)(pos - seq_at - (int64_t)unit * tiles);
-        const int t1 = p.align ? tiles : (int)min((int64_t)tiles, t0 + (hi - pos));
+        const int64_t unit_at = seq_at + (int64_t)unit * cost;
+        const int t0 = max(0, (int)(pos - unit_at) - kUnitCost);
+        const int t1 = p.align ? tiles : (int)min((int64_t)tiles, hi - unit_at - kUnitCost);
+        if (t1 <= t0) break;                       // the range ends before the unit's first tile
         const int kvh = unit / groups, x0 = (unit % groups) * NT;
         const int nvalid = min(NT, q.n * p.NG - x0);
         const int32_t* bt = a.c.bt + (int64_t)s * a.c.max_pages;
@@ -768,13 +802,13 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
           }
           int rows = 0;
           auto head_of = [&](int r, int& tok) {    // head within the kv head's, and token, of row r
-            const int x = x0 + r / 8;
+            const int x = x0 + r / RG;
             tok = p.by_NG.quot(x);
-            return (x - tok * p.NG) * 8 + r % 8;
+            return (x - tok * p.NG) * RG + r % RG;
           };
           int tok;
 #pragma unroll 1
-          for (int r = lane; r < nvalid * 8; r += 32) rows += head_of(r, tok) < p.G;
+          for (int r = lane; r < nvalid * RG; r += 32) rows += head_of(r, tok) < p.G;
           rows = __reduce_add_sync(0xffffffffu, rows);
           if (lane == 0) {
             Piece d;
@@ -783,12 +817,12 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
             d.len = q.len; d.n = q.n; d.bos = q.bos; d.x0 = x0; d.nvalid = nvalid; d.kvh = kvh;
             *piece = d;
             if (t0 == 0 && t1 < tiles)
-              rec = {1, q.bos, x0, nvalid, kvh, rg.before(pos + tiles) - (int)blockIdx.x};
+              rec = {1, q.bos, x0, nvalid, kvh, rg.before(unit_at + cost) - (int)blockIdx.x};
             tc::mbar_arrive_expect_tx(qfull, (uint32_t)(rows * D * sizeof(T)));
           }
           __syncwarp();
 #pragma unroll 1
-          for (int r = lane; r < nvalid * 8; r += 32) {
+          for (int r = lane; r < nvalid * RG; r += 32) {
             const int h = head_of(r, tok);
             if (h < p.G) {
               tc::bulk_load(qs + r * C::QPITCH,
@@ -805,7 +839,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
           ++npiece;
         }
         if (!ok) break;
-        pos += t1 - t0;
+        pos = unit_at + cost;
         ++unit;
       }
     }
@@ -839,7 +873,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
     if (q.n > 0 && q.len == 0) zero_rows(a, q);
   }
   const int tw = warp % C::TG;                     // which slices; warps tw + k TG share them
-  typename WarpOf<T, D, NT>::type w;
+  typename WarpOf<T, D, NT, RG>::type w;
   int it = 0;
   // After a wait that ran out a warp carries on with what the stages hold until the next
   // barrier of all consumers, where they agree to stop: no barrier is left short of a warp.
@@ -857,7 +891,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
     if (d.tile0 < 0) break;
     w.start(qs, warp / C::TG, xs + tw * 2 * (C::XW + C::XA), lane);
     __syncwarp();
-    if (lane == 0) tc::mbar_arrive(qempty);
+    if (decltype(w)::QREG && lane == 0) tc::mbar_arrive(qempty);
     auto lim = [&](int nt) { return d.len - d.n + p.by_NG.quot(d.x0 + min(nt, d.nvalid - 1)) + 1; };
     const int most = lim(NT - 1);
     bool any = false;
@@ -892,7 +926,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
       break;
     }
     // a thread per row: each share's weight in the row (in place of its maximum)
-    if (tid < d.nvalid * 8) {
+    if (tid < d.nvalid * RG) {
       float mt = -INFINITY, lt = 0.f, f[C::TG];
 #pragma unroll
       for (int k = 0; k < C::TG; ++k) mt = fmaxf(mt, jm[k * C::ROWS + tid]);
@@ -920,7 +954,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
         y[2] = fmaf(v.z, f, y[2]); y[3] = fmaf(v.w, f, y[3]);
       }
     };
-    const int groups4 = d.nvalid * 8 * (D / 4);
+    const int groups4 = d.nvalid * RG * (D / 4);
     if (d.slot >= 0) {
       float* po = p.part_o + (int64_t)d.slot * C::ROWS * D;
 #pragma unroll 4
@@ -932,7 +966,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
     } else {
       // the next four columns' gate loaded ahead
       auto place = [&](int i, int& tok) {          // head of group i (-1: no such row), and token
-        const int r = i / (D / 4), x = d.x0 + r / 8, t = p.by_NG.quot(x), h = (x - t * p.NG) * 8 + r % 8;
+        const int r = i / (D / 4), x = d.x0 + r / RG, t = p.by_NG.quot(x), h = (x - t * p.NG) * RG + r % RG;
         tok = d.bos + t;
         return i < groups4 && h < p.G ? d.kvh * p.G + h : -1;
       };
@@ -956,6 +990,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
       }
     }
     tc::named_sync(1, C::CW * 32);
+    if (!decltype(w)::QREG && lane == 0) tc::mbar_arrive(qempty);
   }
 }
 
@@ -1020,8 +1055,9 @@ paged_attn_join_kernel(const __grid_constant__ Params p, int ctas, int rows) {
   const int lane = threadIdx.x & 31, k0 = lane / (32 / PG);
   const int i = (blockIdx.y * (kJoinThreads / 32) + (threadIdx.x >> 5)) * (32 / PG) + lane % (32 / PG);
   const int row = i / (D / 4), e = (i % (D / 4)) * 4;
-  const int x = r.x0 + row / 8, t = p.by_NG.quot(x), h = (x - t * p.NG) * 8 + row % 8;
-  const bool live = r.valid && row < r.nvalid * 8 && h < p.G;
+  const int oct = row >> p.rg_log, x = r.x0 + oct, t = p.by_NG.quot(x);
+  const int h = ((x - t * p.NG - oct) << p.rg_log) + row;
+  const bool live = r.valid && oct < r.nvalid && h < p.G;
   if (!__any_sync(0xffffffffu, live)) return;
   float gt[4], m = -INFINITY, l = 0.f, y[4] = {0.f, 0.f, 0.f, 0.f};
   if (live && k0 == 0) gate4<T>(p.a, r.bos + t, r.kvh * p.G + h, e, gt);
@@ -1088,8 +1124,9 @@ paged_attn_join_few_kernel(const __grid_constant__ Params p, int ctas) {
   const int c0 = nth_record<kFewThreads>(p, ctas, blockIdx.x, found);
   if (c0 < 0) return;
   const SplitRec r = p.rec[c0];
-  const int row = blockIdx.y, x = r.x0 + row / 8, t = p.by_NG.quot(x), h = (x - t * p.NG) * 8 + row % 8;
-  if (row >= r.nvalid * 8 || h >= p.G) return;
+  const int row = blockIdx.y, oct = row >> p.rg_log, x = r.x0 + oct, t = p.by_NG.quot(x);
+  const int h = ((x - t * p.NG - oct) << p.rg_log) + row;
+  if (oct >= r.nvalid || h >= p.G) return;
   constexpr int U = 5;                             // (two units over 304 CTAs: all of their 152 pieces at once)
   const int k = tid / LPR, col = (tid % LPR) * 4, e = blockIdx.z * 64 + col, n = r.pieces;
   float v[U][4];
@@ -1177,10 +1214,10 @@ bool cache_map(CUtensorMap* map, const void* base, const PagedAttnArgs& a, int c
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <typename T, int D, int NT>
+template <typename T, int D, int NT, int RG = 8>
 cudaError_t launch_c(const PagedAttnArgs& a, cudaStream_t s) {
-  using C = Cfg<T, D, NT>;
-  const auto fn = paged_attn_kernel<T, D, NT>;
+  using C = Cfg<T, D, NT, RG>;
+  const auto fn = paged_attn_kernel<T, D, NT, RG>;
   static bool ready[64] = {false};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -1194,7 +1231,8 @@ cudaError_t launch_c(const PagedAttnArgs& a, cudaStream_t s) {
   Params p{};
   p.a = a;
   p.G = a.Nq / a.Nkv;
-  p.NG = (p.G + 7) / 8;
+  p.NG = (p.G + RG - 1) / RG;
+  p.rg_log = RG == 8 ? 3 : 2;
   p.by_NG = Div::of(p.NG);
   p.by_page = Div::of(a.c.page_size);
   p.box = std::gcd(a.c.page_size, C::TILE);
@@ -1234,6 +1272,13 @@ cudaError_t launch_bf16(const PagedAttnArgs& a, int nt, cudaStream_t s) {
   return launch_c<bf16, D, 4>(a, s);
 }
 
+// Four rows where the kv head has no more: half the arithmetic of eight.  (With more heads
+// than four, eight rows mean fewer passes over the cache.)
+template <int D>
+cudaError_t launch_f32(const PagedAttnArgs& a, cudaStream_t s) {
+  return a.Nq / a.Nkv <= 4 ? launch_c<float, D, 1, 4>(a, s) : launch_c<float, D, 1, 8>(a, s);
+}
+
 }  // namespace
 
 size_t paged_attn_workspace_bytes(int num_seqs, int total, int Nq, int Nkv, int D) {
@@ -1247,8 +1292,7 @@ cudaError_t launch_paged_attn(const PagedAttnArgs& a, cudaStream_t s) {
   const int nt = octets_per_pass(a.num_seqs, a.total, a.Nq, a.Nkv, a.D, a.in_bf16);
   if (a.in_bf16)
     return a.D == 64 ? launch_bf16<64>(a, nt, s) : a.D == 128 ? launch_bf16<128>(a, nt, s) : launch_bf16<256>(a, nt, s);
-  return a.D == 64 ? launch_c<float, 64, 1>(a, s)
-                   : a.D == 128 ? launch_c<float, 128, 1>(a, s) : launch_c<float, 256, 1>(a, s);
+  return a.D == 64 ? launch_f32<64>(a, s) : a.D == 128 ? launch_f32<128>(a, s) : launch_f32<256>(a, s);
 }
 
 }  // namespace gdn
