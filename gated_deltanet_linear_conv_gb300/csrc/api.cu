@@ -639,14 +639,17 @@ int gdn_paged_kv_append(const gdn_attn_dims* dims, const int32_t* cu_seqlens, co
   return norm_rope(fn, dims, cu_seqlens, q, k, v, in_dtype, nr, cache, cache_dtype, q_out, q_dtype, nullptr, stream);
 }
 
-int gdn_paged_attn_decode_workspace_size(const gdn_attn_dims* dims, size_t* bytes) {
+int gdn_paged_attn_decode_workspace_size(const gdn_attn_dims* dims, int in_dtype, int64_t table_tokens,
+                                         size_t* bytes) {
   const char* fn = "gdn_paged_attn_decode_workspace_size";
   if (dims == nullptr || bytes == nullptr) return fail(GDN_ERR_INVALID_ARG, "%s: NULL argument", fn);
+  if (!valid_dtype(in_dtype)) return fail(GDN_ERR_INVALID_ARG, "%s: bad dtype", fn);
+  if (table_tokens < 0) return fail(GDN_ERR_INVALID_ARG, "%s: table_tokens < 0", fn);
   gdn_attn_dims d = *dims;
   if (d.num_seqs > 1) d.num_seqs = 1;            // the bounds come with the call: no equal split required here
   CHECK(check_attn_dims(fn, &d, nullptr));
-  *bytes = gdn::paged_attn_workspace_bytes(dims->num_seqs, dims->total_tokens, dims->num_q_heads,
-                                           dims->num_kv_heads, dims->head_dim);
+  *bytes = gdn::paged_attn_workspace_bytes(dims->num_seqs, dims->total_tokens, dims->num_q_heads, dims->num_kv_heads,
+                                           dims->head_dim, in_dtype == GDN_BF16, table_tokens);
   return GDN_OK;
 }
 
@@ -663,7 +666,8 @@ int gdn_paged_attn_decode(const gdn_attn_dims* dims, const int32_t* cu_seqlens, 
   CHECK(check_cache(fn, dims, cache, in_dtype));
   REQUIRE_PTR(o);
   const size_t need = gdn::paged_attn_workspace_bytes(dims->num_seqs, dims->total_tokens, dims->num_q_heads,
-                                                      dims->num_kv_heads, dims->head_dim);
+                                                      dims->num_kv_heads, dims->head_dim, in_dtype == GDN_BF16,
+                                                      (int64_t)cache->max_pages * cache->page_size);
   if (need > 0 && (workspace == nullptr || workspace_bytes < need || !aligned16(workspace)))
     return fail(GDN_ERR_INVALID_ARG, "%s: workspace of %zu bytes (16-byte aligned) required, got %zu", fn, need,
                 workspace_bytes);

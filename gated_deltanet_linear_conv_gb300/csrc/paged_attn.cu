@@ -1199,6 +1199,11 @@ int octets_per_pass(int num_seqs, int total, int Nq, int Nkv, int D, bool bf) {
   return nt;
 }
 
+// Tables so short that ranges end at unit borders.
+bool short_table(int D, bool bf, int64_t table_tokens) {
+  return table_tokens <= (int64_t)kAlignTiles * (kStageHalf / (D * (bf ? 2 : 4)));
+}
+
 // A 4-D map over the cache, {D, slot, head, page}, box {cols, box, 1, 1}.
 bool cache_map(CUtensorMap* map, const void* base, const PagedAttnArgs& a, int cols, int box) {
   EncodeTiledFn enc = tmap_encoder();
@@ -1236,7 +1241,7 @@ cudaError_t launch_c(const PagedAttnArgs& a, cudaStream_t s) {
   p.by_NG = Div::of(p.NG);
   p.by_page = Div::of(a.c.page_size);
   p.box = std::gcd(a.c.page_size, C::TILE);
-  p.align = ((int64_t)a.c.max_pages * a.c.page_size + C::TILE - 1) / C::TILE <= kAlignTiles;
+  p.align = short_table(D, C::BF, (int64_t)a.c.max_pages * a.c.page_size);
   p.c = a.scale * kLog2e;
   uint8_t* ws = static_cast<uint8_t*>(a.ws);
   p.rec = reinterpret_cast<SplitRec*>(ws);
@@ -1281,9 +1286,9 @@ cudaError_t launch_f32(const PagedAttnArgs& a, cudaStream_t s) {
 
 }  // namespace
 
-size_t paged_attn_workspace_bytes(int num_seqs, int total, int Nq, int Nkv, int D) {
-  // the same for every type and table: the caller may size it before those are known
-  const int rows = octets_per_pass(num_seqs, total, Nq, Nkv, D, true) * 8;
+size_t paged_attn_workspace_bytes(int num_seqs, int total, int Nq, int Nkv, int D, bool bf, int64_t table_tokens) {
+  if (short_table(D, bf, table_tokens)) return 0;
+  const size_t rows = octets_per_pass(num_seqs, total, Nq, Nkv, D, bf) * 8;
   const size_t grid = std::min(kOcc * num_sms(), kMaxCtas);
   return align16(sizeof(SplitRec) * grid) + align16(2 * grid * rows * 2 * 4) + 2 * grid * rows * D * 4;
 }

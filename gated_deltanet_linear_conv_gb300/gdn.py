@@ -94,7 +94,7 @@ _SIGS = {
                           _P, _I, _P], _I),
     'gdn_qk_norm_rope': ([_ADIMS, _P, _HEADS, _HEADS, _I, _NR, _P, _P, _I, _P], _I),
     'gdn_paged_kv_append': ([_ADIMS, _P, _HEADS, _HEADS, _HEADS, _I, _NR, _CACHE, _I, _P, _I, _P], _I),
-    'gdn_paged_attn_decode_workspace_size': ([_ADIMS, ctypes.POINTER(_SZ)], _I),
+    'gdn_paged_attn_decode_workspace_size': ([_ADIMS, _I, _I64, ctypes.POINTER(_SZ)], _I),
     'gdn_paged_attn_decode': ([_ADIMS, _P, _HEADS, _HEADS, _I, _CACHE, _F, _P, _I, _P, _SZ, _P], _I),
     'gdn_test_chunk_wait_timeout': ([_DIMS, _P, _P, _P, _P, _P, _P, _P, _SZ, _I64, _P], _I),
 }
@@ -430,12 +430,13 @@ def _heads(t, what):
     """[tokens, heads, D] with contiguous head rows (a slice of a wider projection is fine)."""
     if t is None:
         return None
-    if t.dim() != 3:
+    shape = t.shape
+    if len(shape) != 3:
         raise ValueError('%s must be [tokens, heads, head_dim]' % what)
     ts, hs, es = t.stride()
     if es != 1:
         raise ValueError('the head rows of %s must be contiguous' % what)
-    T, H, D = t.shape
+    T, H, D = shape
     # a stride over an axis of one entry is never used: any value may stand there
     return _pack_heads(t.data_ptr(), ts if T > 1 else H * D, hs if H > 1 else D)
 
@@ -461,28 +462,27 @@ def _norm_rope(q_norm_w, k_norm_w, norm_eps, cos_sin, positions, interleaved, T,
 
 def _cache(k_cache, v_cache, block_table, kv_lens, Nkv, D, num_seqs):
     """Checks the cache's tensors against the call's sizes and packs them."""
-    shape = k_cache.shape
+    shape, stride = k_cache.shape, k_cache.stride()
     if len(shape) != 4 or v_cache.shape != shape or k_cache.dtype != v_cache.dtype:
         raise ValueError('k_cache and v_cache share the shape [pages, kv heads, page size, head_dim] and a dtype')
     pages, H, P, E = shape
     if H != Nkv or E != D:
         raise ValueError('the cache holds %d heads of %d, the call has %d of %d' % (H, E, Nkv, D))
-    ps, hs, ss, es = stride = k_cache.stride()
-    if es != 1 or (v_cache.stride(3) != 1 and E > 1):
-        raise ValueError('the head rows of the cache must be contiguous')
-    # a stride over an axis of one entry is never used: any value may stand there
+    v_stride = v_cache.stride()
     if pages == 1 or H == 1 or P == 1:
+        # a stride over an axis of one entry is never used: any value may stand there
         def used(st):
-            return (st[0] if pages > 1 else H * P * E, st[1] if H > 1 else P * E, st[2] if P > 1 else E)
-        ps, hs, ss = used(stride)
-        same = used(v_cache.stride()) == (ps, hs, ss)
-    else:
-        same = v_cache.stride() == stride
-    if not same:
+            return (st[0] if pages > 1 else H * P * E, st[1] if H > 1 else P * E, st[2] if P > 1 else E, st[3])
+        stride, v_stride = used(stride), used(v_stride)
+    ps, hs, ss, es = stride
+    if es != 1 or v_stride[3] != 1:
+        raise ValueError('the head rows of the cache must be contiguous')
+    if v_stride != stride:
         raise ValueError('k_cache and v_cache must have the same strides')
-    if block_table.dim() != 2 or block_table.shape[0] != num_seqs or kv_lens.numel() != num_seqs:
+    rows = block_table.shape
+    if len(rows) != 2 or rows[0] != num_seqs or kv_lens.numel() != num_seqs:
         raise ValueError('block_table is [sequences, pages] and kv_lens [sequences]')
-    return _pack_cache(k_cache.data_ptr(), v_cache.data_ptr(), ps, hs, ss, pages, P, block_table.shape[1],
+    return _pack_cache(k_cache.data_ptr(), v_cache.data_ptr(), ps, hs, ss, pages, P, rows[1],
                        _addr(block_table, torch.int32, 'block_table'), _addr(kv_lens, torch.int32, 'kv_lens'))
 
 
@@ -559,16 +559,18 @@ def paged_kv_append(k, v, k_cache, v_cache, block_table, kv_lens, q=None, cos_si
     return q_out if q is not None else None
 
 
-def paged_attn_decode_workspace_size(num_seqs, total, Nq, Nkv, D):
+def paged_attn_decode_workspace_size(num_seqs, total, Nq, Nkv, D, dtype, table_tokens):
+    """Bytes for calls of these sizes and type over tables of up to ``table_tokens`` cache entries."""
     n = _SZ(0)
-    _check(lib().gdn_paged_attn_decode_workspace_size(gdn_attn_dims(num_seqs, total, Nq, Nkv, D), n),
-           'gdn_paged_attn_decode_workspace_size')
+    _check(lib().gdn_paged_attn_decode_workspace_size(gdn_attn_dims(num_seqs, total, Nq, Nkv, D),
+                                                      GDN_BF16 if dtype == torch.bfloat16 else GDN_F32,
+                                                      table_tokens, n), 'gdn_paged_attn_decode_workspace_size')
     return n.value
 
 
 @functools.lru_cache(maxsize=256)
-def _attn_workspace_size(device, num_seqs, total, Nq, Nkv, D):
-    return paged_attn_decode_workspace_size(num_seqs, total, Nq, Nkv, D)
+def _attn_workspace_size(device, *sizes):
+    return paged_attn_decode_workspace_size(*sizes)
 
 
 def paged_attn_decode(q, k_cache, v_cache, block_table, kv_lens, scale=None, gate=None, cu_seqlens=None,
@@ -589,7 +591,8 @@ def paged_attn_decode(q, k_cache, v_cache, block_table, kv_lens, scale=None, gat
     cache = _cache(k_cache, v_cache, block_table, kv_lens, Nkv, D, num_seqs)
     o = _out(o, (T, Nq, D), out_dtype, q.device, 'o')
     if workspace is None:
-        ws_bytes = _attn_workspace_size(q.get_device(), num_seqs, T, Nq, Nkv, D)
+        ws_bytes = _attn_workspace_size(q.get_device(), num_seqs, T, Nq, Nkv, D, q.dtype,
+                                        block_table.shape[1] * k_cache.shape[2])
         if ws_bytes > 0:
             workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=q.device)
     else:

@@ -502,9 +502,13 @@ int gdn_paged_kv_append(const gdn_attn_dims* dims, const int32_t* cu_seqlens,
  *   o          [tokens, Nq, D]   out_dtype, contiguous
  *   workspace  device scratch of gdn_paged_attn_decode_workspace_size() bytes
  *              (may be NULL when that is 0), no initialisation needed; not to
- *              be shared by calls that can run at the same time
+ *              be shared by calls that can run at the same time.  The size is
+ *              for the current device and for tables of up to table_tokens =
+ *              max_pages * page_size cache entries: it is 0 for short tables,
+ *              and the same for all others.
  * ------------------------------------------------------------------------ */
-int gdn_paged_attn_decode_workspace_size(const gdn_attn_dims* dims, size_t* bytes);
+int gdn_paged_attn_decode_workspace_size(const gdn_attn_dims* dims, int in_dtype, int64_t table_tokens,
+                                         size_t* bytes);
 
 int gdn_paged_attn_decode(const gdn_attn_dims* dims, const int32_t* cu_seqlens,
                           const gdn_heads* q, const gdn_heads* gate, int in_dtype,

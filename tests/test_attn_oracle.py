@@ -137,6 +137,12 @@ def test_refusals(gdn, call, kw, code, word):
     assert word in gdn.lib().gdn_last_error_string().decode(), gdn.lib().gdn_last_error_string()
 
 
+def test_workspace_too_small_is_refused(gdn):
+    big = dict(maxp=4096)                              # tables of 65536 entries
+    assert _attn(gdn, wsb=16, **big) == _attn(gdn, ws=None, **big) == _attn(gdn, ws=X + 8, **big) == gdn.GDN_ERR_INVALID_ARG
+    assert b'workspace' in gdn.lib().gdn_last_error_string()
+
+
 def test_no_tokens_is_no_work(gdn):
     assert _rope(gdn, T=0) == _append(gdn, T=0) == _attn(gdn, T=0) == gdn.GDN_OK
 
@@ -144,7 +150,14 @@ def test_no_tokens_is_no_work(gdn):
 def test_null_structs(gdn):
     L = gdn.lib()
     n = ctypes.c_size_t(0)
-    assert L.gdn_paged_attn_decode_workspace_size(None, n) == gdn.GDN_ERR_INVALID_ARG
+    size = L.gdn_paged_attn_decode_workspace_size
+    d = gdn.gdn_attn_dims(3, 7, 8, 2, 128)
+    assert size(None, 0, 64, n) == size(d, 0, 64, None) == size(d, 3, 64, n) == size(d, 0, -1, n) == gdn.GDN_ERR_INVALID_ARG
+    assert size(gdn.gdn_attn_dims(3, 7, 8, 2, 96), 0, 64, n) == gdn.GDN_ERR_UNSUPPORTED
+    assert size(d, 0, 64, n) == gdn.GDN_OK and n.value == 0           # short tables need none
+    assert size(d, 0, 100000, n) == gdn.GDN_OK and n.value > 0
+    short = n.value
+    assert size(d, 0, 1 << 40, n) == gdn.GDN_OK and n.value == short
     assert L.gdn_paged_attn_decode(None, None, None, None, 0, None, 1.0, None, 0, None, 0, None) == gdn.GDN_ERR_INVALID_ARG
     assert _rope(gdn, nr=False) == gdn.GDN_ERR_INVALID_ARG
 

@@ -520,7 +520,8 @@ def test_same_call_twice_is_bit_equal():
     c.v.copy_(rand(92, *c.v.shape))
     q = rand(93, 5, 16, 128)
     y = run_attn(c, q, lens, [1] * 5)
-    ws = torch.full((max(16, gdn.paged_attn_decode_workspace_size(5, 5, 16, 2, 128)),), 255, dtype=torch.uint8, device='cuda')
+    n = gdn.paged_attn_decode_workspace_size(5, 5, 16, 2, 128, BF, c.bt.shape[1] * c.P)
+    ws = torch.full((n,), 255, dtype=torch.uint8, device='cuda')
     for _ in range(5):
         assert torch.equal(run_attn(c, q, lens, [1] * 5, workspace=ws), y)
 
