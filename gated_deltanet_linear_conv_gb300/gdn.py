@@ -405,31 +405,33 @@ def _fn(name):
     return f
 
 
-def _on_device(first, *tensors):
-    """The library launches on the current device: every tensor has to live there."""
-    dev = first.get_device()
+def _device(t):
+    """The library launches on the current device: the index of t's, which has to be that one."""
+    dev = t.get_device()
     if dev < 0 or dev != torch._C._cuda_getDevice():
         raise ValueError('expected CUDA tensors on the current device')
-    for t in tensors:
-        if t is not None and t.get_device() != dev:
-            raise ValueError('expected CUDA tensors on the current device')
+    return dev
 
 
-def _addr(t, dtype, what):
-    """Address of an optional contiguous tensor of the given type (0: none)."""
+def _arg(t, dtype, dev, what):
+    """Address of an optional contiguous tensor of the given type on device ``dev`` (0: none)."""
     if t is None:
         return 0
-    if t.dtype != dtype:
+    if t.get_device() != dev:
+        raise ValueError('%s must be on the device of the other tensors' % what)
+    if t.dtype is not dtype:
         raise ValueError('%s must be %s' % (what, str(dtype)[6:]))
     if not t.is_contiguous():
         raise ValueError('%s must be contiguous' % what)
     return t.data_ptr()
 
 
-def _heads(t, what):
+def _heads(t, dev, what):
     """[tokens, heads, D] with contiguous head rows (a slice of a wider projection is fine)."""
     if t is None:
         return None
+    if t.get_device() != dev:
+        raise ValueError('%s must be on the device of the other tensors' % what)
     shape = t.shape
     if len(shape) != 3:
         raise ValueError('%s must be [tokens, heads, head_dim]' % what)
@@ -441,30 +443,31 @@ def _heads(t, what):
     return _pack_heads(t.data_ptr(), ts if T > 1 else H * D, hs if H > 1 else D)
 
 
-def _norm_rope(q_norm_w, k_norm_w, norm_eps, cos_sin, positions, interleaved, T, D):
-    rot = maxpos = 0
+def _norm_rope(q_norm_w, k_norm_w, norm_eps, cos_sin, positions, interleaved, T, D, dev):
+    rot = maxpos = table = 0
     if cos_sin is not None:
+        table = _arg(cos_sin, torch.float32, dev, 'cos_sin')
         if cos_sin.dim() != 2:
             raise ValueError('cos_sin must be [positions, rotary_dim]')
         maxpos, rot = cos_sin.shape
         if rot == 0:
-            maxpos = 0
-    for w in (q_norm_w, k_norm_w):
-        if w is not None and w.numel() != D:
-            raise ValueError('a norm weight has head_dim elements')
+            maxpos = table = 0
+    if (q_norm_w is not None and q_norm_w.numel() != D) or (k_norm_w is not None and k_norm_w.numel() != D):
+        raise ValueError('a norm weight has head_dim elements')
     if positions is not None and positions.numel() != T:
         raise ValueError('positions has one entry per token')
-    return _pack_norm_rope(_addr(q_norm_w, torch.float32, 'q_norm_w'), _addr(k_norm_w, torch.float32, 'k_norm_w'),
-                           norm_eps, rot, 1 if interleaved else 0, maxpos,
-                           _addr(cos_sin, torch.float32, 'cos_sin') if rot else 0,
-                           _addr(positions, torch.int32, 'positions'))
+    return _pack_norm_rope(_arg(q_norm_w, torch.float32, dev, 'q_norm_w'), _arg(k_norm_w, torch.float32, dev, 'k_norm_w'),
+                           norm_eps, rot, 1 if interleaved else 0, maxpos, table,
+                           _arg(positions, torch.int32, dev, 'positions'))
 
 
-def _cache(k_cache, v_cache, block_table, kv_lens, Nkv, D, num_seqs):
+def _cache(k_cache, v_cache, block_table, kv_lens, Nkv, D, num_seqs, dev):
     """Checks the cache's tensors against the call's sizes and packs them."""
     shape, stride = k_cache.shape, k_cache.stride()
-    if len(shape) != 4 or v_cache.shape != shape or k_cache.dtype != v_cache.dtype:
+    if len(shape) != 4 or v_cache.shape != shape or k_cache.dtype is not v_cache.dtype:
         raise ValueError('k_cache and v_cache share the shape [pages, kv heads, page size, head_dim] and a dtype')
+    if k_cache.get_device() != dev or v_cache.get_device() != dev:
+        raise ValueError('the cache must be on the device of the other tensors')
     pages, H, P, E = shape
     if H != Nkv or E != D:
         raise ValueError('the cache holds %d heads of %d, the call has %d of %d' % (H, E, Nkv, D))
@@ -483,14 +486,13 @@ def _cache(k_cache, v_cache, block_table, kv_lens, Nkv, D, num_seqs):
     if len(rows) != 2 or rows[0] != num_seqs or kv_lens.numel() != num_seqs:
         raise ValueError('block_table is [sequences, pages] and kv_lens [sequences]')
     return _pack_cache(k_cache.data_ptr(), v_cache.data_ptr(), ps, hs, ss, pages, P, rows[1],
-                       _addr(block_table, torch.int32, 'block_table'), _addr(kv_lens, torch.int32, 'kv_lens'))
+                       _arg(block_table, torch.int32, dev, 'block_table'), _arg(kv_lens, torch.int32, dev, 'kv_lens'))
 
 
-def _out(t, shape, dtype, device, what):
-    if t is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    if tuple(t.shape) != shape or not t.is_contiguous():
-        raise ValueError('%s must be contiguous and have the shape %s' % (what, shape))
+def _given(t, shape, dev, what):
+    """An output the caller supplied."""
+    if t.shape != shape or not t.is_contiguous() or t.get_device() != dev:
+        raise ValueError('%s must be contiguous, on the device of the other tensors and of shape %s' % (what, shape))
     return t
 
 
@@ -498,26 +500,30 @@ def qk_norm_rope(q, k=None, cos_sin=None, q_norm_w=None, k_norm_w=None, position
                  num_seqs=1, norm_eps=1e-6, interleaved=False, out_dtype=torch.bfloat16, q_out=None, k_out=None):
     """gdn_qk_norm_rope: per-head RMSNorm and rotation of q [tokens, Nq, D] and k [tokens, Nkv, D].
     Returns (q_out, k_out); ``positions`` default to each token's index in its sequence."""
-    T, Nq, D = q.shape
-    Nkv = Nq
+    T, Nq, D = shape = q.shape
+    Nkv, k_shape = Nq, None
     if k is not None:
         Nkv = k.shape[1]
-        if k.shape != (T, Nkv, D) or k.dtype != q.dtype:
+        k_shape = (T, Nkv, D)
+        if k.shape != k_shape or k.dtype is not q.dtype:
             raise ValueError('q and k share tokens, head_dim and dtype')
-    _on_device(q, k, cos_sin, q_norm_w, k_norm_w, positions, cu_seqlens, q_out, k_out)
+    dev = _device(q)
     cu = 0
     if cu_seqlens is not None:
-        cu = _addr(cu_seqlens, torch.int32, 'cu_seqlens')
+        cu = _arg(cu_seqlens, torch.int32, dev, 'cu_seqlens')
         num_seqs = cu_seqlens.numel() - 1
-    q_out = _out(q_out, (T, Nq, D), out_dtype, q.device, 'q_out')
+    q_out = torch.empty(shape, dtype=out_dtype, device=q.device) if q_out is None else _given(q_out, shape, dev, 'q_out')
+    ko = 0
     if k is not None:
-        k_out = _out(k_out, (T, Nkv, D), q_out.dtype, q.device, 'k_out')
-        if k_out.dtype != q_out.dtype:
+        k_out = (torch.empty(k_shape, dtype=q_out.dtype, device=q.device) if k_out is None
+                 else _given(k_out, k_shape, dev, 'k_out'))
+        if k_out.dtype is not q_out.dtype:
             raise ValueError('q_out and k_out share a dtype')
+        ko = k_out.data_ptr()
     st = _fn('gdn_qk_norm_rope')(
-        _pack_dims(num_seqs, T, Nq, Nkv, D), cu, _heads(q, 'q'), _heads(k, 'k'), _dt(q),
-        _norm_rope(q_norm_w, k_norm_w, norm_eps, cos_sin, positions, interleaved, T, D), q_out.data_ptr(),
-        k_out.data_ptr() if k is not None else 0, _dt(q_out), _stream())
+        _pack_dims(num_seqs, T, Nq, Nkv, D), cu, _heads(q, dev, 'q'), _heads(k, dev, 'k'), _dt(q),
+        _norm_rope(q_norm_w, k_norm_w, norm_eps, cos_sin, positions, interleaved, T, D, dev), q_out.data_ptr(),
+        ko, _dt(q_out), _stream())
     if st:
         _check(st, 'gdn_qk_norm_rope')
     return q_out, k_out
@@ -529,30 +535,29 @@ def paged_kv_append(k, v, k_cache, v_cache, block_table, kv_lens, q=None, cos_si
     """gdn_paged_kv_append: k (normed and rotated on the way) and v of the new tokens into the cache, in place.
     k_cache, v_cache are [pages, Nkv, page size, D] (a [pages, page size, Nkv, D] cache goes in transposed);
     kv_lens include the new tokens.  Returns the normed and rotated q (None without q)."""
-    T, Nkv, D = k.shape
-    if v.shape != k.shape or v.dtype != k.dtype:
+    T, Nkv, D = shape = k.shape
+    if v.shape != shape or v.dtype is not k.dtype:
         raise ValueError('k and v share a shape and a dtype')
-    Nq = Nkv
-    if q is not None:
-        Nq = q.shape[1]
-        if q.shape != (T, Nq, D) or q.dtype != k.dtype:
-            raise ValueError('q shares tokens, head_dim and dtype with k')
-    _on_device(k, v, k_cache, v_cache, block_table, kv_lens, q, cos_sin, q_norm_w, k_norm_w, positions,
-               cu_seqlens, q_out)
+    dev = _device(k)
     num_seqs = kv_lens.numel()
     cu = 0
     if cu_seqlens is not None:
-        cu = _addr(cu_seqlens, torch.int32, 'cu_seqlens')
+        cu = _arg(cu_seqlens, torch.int32, dev, 'cu_seqlens')
         if cu_seqlens.numel() != num_seqs + 1:
             raise ValueError('cu_seqlens has one entry more than kv_lens')
-    cache = _cache(k_cache, v_cache, block_table, kv_lens, Nkv, D, num_seqs)
-    qo, qdt = 0, GDN_BF16
+    cache = _cache(k_cache, v_cache, block_table, kv_lens, Nkv, D, num_seqs, dev)
+    Nq, qo, qdt = Nkv, 0, GDN_BF16
     if q is not None:
-        q_out = _out(q_out, (T, Nq, D), out_dtype, q.device, 'q_out')
+        q_shape = q.shape
+        Nq = q_shape[1]
+        if q_shape != (T, Nq, D) or q.dtype is not k.dtype:
+            raise ValueError('q shares tokens, head_dim and dtype with k')
+        q_out = (torch.empty(q_shape, dtype=out_dtype, device=q.device) if q_out is None
+                 else _given(q_out, q_shape, dev, 'q_out'))
         qo, qdt = q_out.data_ptr(), _dt(q_out)
     st = _fn('gdn_paged_kv_append')(
-        _pack_dims(num_seqs, T, Nq, Nkv, D), cu, _heads(q, 'q'), _heads(k, 'k'), _heads(v, 'v'), _dt(k),
-        _norm_rope(q_norm_w, k_norm_w, norm_eps, cos_sin, positions, interleaved, T, D), cache, _dt(k_cache),
+        _pack_dims(num_seqs, T, Nq, Nkv, D), cu, _heads(q, dev, 'q'), _heads(k, dev, 'k'), _heads(v, dev, 'v'), _dt(k),
+        _norm_rope(q_norm_w, k_norm_w, norm_eps, cos_sin, positions, interleaved, T, D, dev), cache, _dt(k_cache),
         qo, qdt, _stream())
     if st:
         _check(st, 'gdn_paged_kv_append')
@@ -577,30 +582,32 @@ def paged_attn_decode(q, k_cache, v_cache, block_table, kv_lens, scale=None, gat
                       out_dtype=torch.bfloat16, o=None, workspace=None):
     """gdn_paged_attn_decode: attention of the new tokens q [tokens, Nq, D] (one or a few per sequence, bounds
     from cu_seqlens, else equally many) over the cache, times sigmoid(gate) when given.  Returns o."""
-    T, Nq, D = q.shape
-    if k_cache.dtype != q.dtype or (gate is not None and (gate.dtype != q.dtype or gate.shape != q.shape)):
+    T, Nq, D = shape = q.shape
+    dtype = q.dtype
+    if k_cache.dtype is not dtype or (gate is not None and (gate.dtype is not dtype or gate.shape != shape)):
         raise ValueError('q, gate and the cache share a dtype; gate has the shape of q')
-    _on_device(q, k_cache, v_cache, block_table, kv_lens, gate, cu_seqlens, o, workspace)
+    dev = _device(q)
     num_seqs = kv_lens.numel()
     cu = 0
     if cu_seqlens is not None:
-        cu = _addr(cu_seqlens, torch.int32, 'cu_seqlens')
+        cu = _arg(cu_seqlens, torch.int32, dev, 'cu_seqlens')
         if cu_seqlens.numel() != num_seqs + 1:
             raise ValueError('cu_seqlens has one entry more than kv_lens')
     Nkv = k_cache.shape[1]
-    cache = _cache(k_cache, v_cache, block_table, kv_lens, Nkv, D, num_seqs)
-    o = _out(o, (T, Nq, D), out_dtype, q.device, 'o')
+    cache = _cache(k_cache, v_cache, block_table, kv_lens, Nkv, D, num_seqs, dev)
+    o = torch.empty(shape, dtype=out_dtype, device=q.device) if o is None else _given(o, shape, dev, 'o')
+    ws = 0
     if workspace is None:
-        ws_bytes = _attn_workspace_size(q.get_device(), num_seqs, T, Nq, Nkv, D, q.dtype,
-                                        block_table.shape[1] * k_cache.shape[2])
+        ws_bytes = _attn_workspace_size(dev, num_seqs, T, Nq, Nkv, D, dtype, block_table.shape[1] * k_cache.shape[2])
         if ws_bytes > 0:
             workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=q.device)
+            ws = workspace.data_ptr()
     else:
         ws_bytes = workspace.numel() * workspace.element_size()
+        ws = _given(workspace, workspace.shape, dev, 'workspace').data_ptr()
     st = _fn('gdn_paged_attn_decode')(
-        _pack_dims(num_seqs, T, Nq, Nkv, D), cu, _heads(q, 'q'), _heads(gate, 'gate'), _dt(q), cache,
-        1.0 / math.sqrt(D) if scale is None else scale, o.data_ptr(), _dt(o),
-        0 if workspace is None else workspace.data_ptr(), ws_bytes, _stream())
+        _pack_dims(num_seqs, T, Nq, Nkv, D), cu, _heads(q, dev, 'q'), _heads(gate, dev, 'gate'), _dt(q), cache,
+        1.0 / math.sqrt(D) if scale is None else scale, o.data_ptr(), _dt(o), ws, ws_bytes, _stream())
     if st:
         _check(st, 'gdn_paged_attn_decode')
     return o

@@ -184,22 +184,22 @@ def test_binding_refusals(gdn):
     with pytest.raises(ValueError, match='dtype'):
         gdn.paged_attn_decode(q, kc.float(), kc.float(), bt, lens)
     with pytest.raises(ValueError, match='shape'):
-        gdn._cache(kc, kc[:2], bt, lens, 2, 64, 2)
+        gdn._cache(kc, kc[:2], bt, lens, 2, 64, 2, -1)
     with pytest.raises(ValueError, match='heads'):
-        gdn._cache(kc, kc, bt, lens, 4, 64, 2)
+        gdn._cache(kc, kc, bt, lens, 4, 64, 2, -1)
     with pytest.raises(ValueError, match='contiguous'):
-        gdn._cache(kc.transpose(2, 3).contiguous().transpose(2, 3), kc, bt, lens, 2, 64, 2)
+        gdn._cache(kc.transpose(2, 3).contiguous().transpose(2, 3), kc, bt, lens, 2, 64, 2, -1)
     with pytest.raises(ValueError, match='strides'):
-        gdn._cache(kc, torch.zeros(3, 16, 2, 64, dtype=bf).transpose(1, 2), bt, lens, 2, 64, 2)
+        gdn._cache(kc, torch.zeros(3, 16, 2, 64, dtype=bf).transpose(1, 2), bt, lens, 2, 64, 2, -1)
     with pytest.raises(ValueError, match='block_table'):
-        gdn._cache(kc, kc, bt, lens[:1], 2, 64, 2)
+        gdn._cache(kc, kc, bt, lens[:1], 2, 64, 2, -1)
     with pytest.raises(ValueError, match='int32'):
-        gdn._cache(kc, kc, bt, lens.long(), 2, 64, 2)
+        gdn._cache(kc, kc, bt, lens.long(), 2, 64, 2, -1)
     with pytest.raises(ValueError, match='contiguous'):
-        gdn._cache(kc, kc, torch.zeros(1, 2, dtype=torch.int32).T.expand(2, 2), lens, 2, 64, 2)
+        gdn._cache(kc, kc, torch.zeros(1, 2, dtype=torch.int32).T.expand(2, 2), lens, 2, 64, 2, -1)
     with pytest.raises(ValueError, match='contiguous'):
-        gdn._heads(torch.zeros(2, 64, 8).transpose(1, 2), 'q')
+        gdn._heads(torch.zeros(2, 64, 8).transpose(1, 2), -1, 'q')
     with pytest.raises(ValueError, match='norm weight'):
-        gdn._norm_rope(torch.zeros(32), None, 1e-6, None, None, False, 2, 64)
+        gdn._norm_rope(torch.zeros(32), None, 1e-6, None, None, False, 2, 64, -1)
     with pytest.raises(ValueError, match='share'):
         gdn.qk_norm_rope(q, q.float())
