@@ -131,6 +131,30 @@ int check_norm_rope(const char* fn, const gdn_attn_dims* d, const gdn_norm_rope*
   return GDN_OK;
 }
 
+// The cache's axes 0 slot, 1 head, 2 page by increasing stride; axes of one entry last, with
+// the largest stride of the others.
+void cache_axes(const gdn_paged_cache* c, int num_kv_heads, int head_dim, int order[3], int64_t stride[3]) {
+  const int64_t st[3] = {c->slot_stride, c->head_stride, c->page_stride};
+  const int ext[3] = {c->page_size, num_kv_heads, c->num_pages};
+  int n = 0;
+  for (int i = 0; i < 3; ++i) {
+    if (ext[i] <= 1) continue;
+    int j = n++;
+    for (; j > 0 && stride[j - 1] > st[i]; --j) {
+      stride[j] = stride[j - 1];
+      order[j] = order[j - 1];
+    }
+    stride[j] = st[i];
+    order[j] = i;
+  }
+  const int64_t top = n > 0 ? stride[n - 1] : head_dim;
+  for (int i = 0; i < 3; ++i) {
+    if (ext[i] > 1) continue;
+    stride[n] = top;
+    order[n++] = i;
+  }
+}
+
 int check_cache(const char* fn, const gdn_attn_dims* d, const gdn_paged_cache* c, int dtype) {
   if (c == nullptr) return fail(GDN_ERR_INVALID_ARG, "%s: cache is NULL", fn);
   const void *cache_k = c->k, *cache_v = c->v;
@@ -147,8 +171,18 @@ int check_cache(const char* fn, const gdn_attn_dims* d, const gdn_paged_cache* c
     if (st[i] <= 0 || st[i] % unit != 0 || st[i] >= most)
       return fail(GDN_ERR_INVALID_ARG, "%s: the cache strides must be positive multiples of 16 bytes below 2^40 bytes",
                   fn);
-  if (c->slot_stride < d->head_dim)
-    return fail(GDN_ERR_INVALID_ARG, "%s: the cache's slot_stride is below head_dim", fn);
+  const int ext[3] = {c->page_size, d->num_kv_heads, c->num_pages};
+  int order[3];
+  int64_t stride[3], span = d->head_dim;
+  cache_axes(c, d->num_kv_heads, d->head_dim, order, stride);
+  for (int i = 0; i < 3 && ext[order[i]] > 1; ++i) {
+    if (stride[i] < span) return fail(GDN_ERR_INVALID_ARG, "%s: the cache's strides make entries overlap", fn);
+    if (i > 0 && stride[i] % stride[i - 1] != 0)
+      return fail(GDN_ERR_UNSUPPORTED, "%s: the cache's strides are not multiples of one another", fn);
+    span = stride[i] * ext[order[i]];
+    if (span / ext[order[i]] != stride[i] || span > ((int64_t)1 << 60))
+      return fail(GDN_ERR_INVALID_ARG, "%s: the cache's strides span more than 2^60 elements", fn);
+  }
   return GDN_OK;
 }
 
@@ -156,9 +190,11 @@ gdn::HeadsIn heads_in(const gdn_heads* h) {
   return h == nullptr ? gdn::HeadsIn{nullptr, 0, 0} : gdn::HeadsIn{h->data, h->token_stride, h->head_stride};
 }
 
-gdn::PagedCache paged_cache(const gdn_paged_cache* c) {
-  return {c->k, c->v, c->page_stride, c->head_stride, c->slot_stride, c->block_table, c->kv_lens,
-          c->num_pages, c->page_size, c->max_pages};
+gdn::PagedCache paged_cache(const gdn_attn_dims* d, const gdn_paged_cache* c) {
+  gdn::PagedCache p{c->k, c->v, c->page_stride, c->head_stride, c->slot_stride, c->block_table, c->kv_lens,
+                    c->num_pages, c->page_size, c->max_pages, {}, {}};
+  cache_axes(c, d->num_kv_heads, d->head_dim, p.order, p.sorted);
+  return p;
 }
 
 #define CHECK(call)                   \
@@ -189,7 +225,7 @@ int norm_rope(const char* fn, const gdn_attn_dims* dims, const int32_t* cu, cons
   gdn::NormRopeArgs p{};
   p.q = heads_in(q); p.k = heads_in(k); p.v = heads_in(v);
   p.q_out = q_out; p.k_out = k_out;
-  if (cache != nullptr) p.c = paged_cache(cache);
+  if (cache != nullptr) p.c = paged_cache(dims, cache);
   if (nr != nullptr) {
     p.qw = nr->q_norm_w; p.kw = nr->k_norm_w; p.eps = nr->norm_eps;
     p.rot = nr->rotary_dim; p.inter = nr->interleaved; p.max_pos = nr->max_positions;
@@ -674,7 +710,7 @@ int gdn_paged_attn_decode(const gdn_attn_dims* dims, const int32_t* cu_seqlens, 
   int* flag = nullptr;
   CHECK(get_flag(&flag));
   gdn::PagedAttnArgs p{};
-  p.q = heads_in(q); p.gate = heads_in(gate); p.c = paged_cache(cache); p.o = o;
+  p.q = heads_in(q); p.gate = heads_in(gate); p.c = paged_cache(dims, cache); p.o = o;
   p.cu = cu_seqlens; p.num_seqs = dims->num_seqs; p.total = dims->total_tokens;
   p.Nq = dims->num_q_heads; p.Nkv = dims->num_kv_heads; p.D = dims->head_dim;
   p.scale = scale; p.in_bf16 = in_dtype == GDN_BF16; p.out_bf16 = out_dtype == GDN_BF16;

@@ -114,6 +114,10 @@ struct PagedCache {
   const int32_t* bt;                             // [N, max_pages]
   const int32_t* lens;                           // [N]
   int num_pages, page_size, max_pages;
+  // the axes 0 slot, 1 head, 2 page by increasing stride, and those strides (of an axis with
+  // one entry, whose stride is never used: one that fits the order)
+  int order[3];
+  int64_t sorted[3];
 };
 
 struct NormRopeArgs {

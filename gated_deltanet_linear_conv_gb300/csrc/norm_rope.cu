@@ -283,14 +283,15 @@ cudaError_t launch_d(const NormRopeArgs& p, cudaStream_t s) {
   // blocks of 48 rows, take 29.4 us in two ranges, just over one round, and 25.2 us in three.)
   int span = rows;
   int64_t best = INT64_MAX;
+  const int64_t round = (int64_t)kResident * num_sms();
   for (int r = 1; r <= std::min(rows, 64); ++r) {
     const int s_r = (rows + r - 1) / r, used = (rows + s_r - 1) / s_r;
-    const int64_t round = (int64_t)kResident * num_sms();
     const int64_t cost = ((int64_t)tblocks * used + round - 1) / round * (kSetup + s_r);
     if (cost < best) {
       best = cost;
       span = s_r;
     }
+    if ((int64_t)tblocks * used >= 16 * round) break;              // more rounds than that differ little
   }
   const Div by_len = Div::of(std::max(1, p.total / p.num_seqs)), by_page = Div::of(std::max(1, p.c.page_size));
   const dim3 grid(tblocks, (rows + span - 1) / span);

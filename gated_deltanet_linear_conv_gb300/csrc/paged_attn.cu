@@ -171,7 +171,7 @@ __device__ __forceinline__ float rcp(float x) {
   return y;
 }
 
-// One box of the 4-D map {D, slot, kv head, page}.
+// One box of a 4-D map.
 __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, uint64_t* bar, int x, int y, int z, int w) {
   asm volatile(
       "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(
@@ -782,11 +782,12 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
 #pragma unroll 1
           for (int b = lane; b < nbox; b += 32) {
             if (b >= 32) lookup(tile, b, page, off);
+            auto axis = [&](int i) { return a.c.order[i] == 0 ? off : a.c.order[i] == 1 ? kvh : page; };
 #pragma unroll
             for (int cb = 0; cb < CB; ++cb) {
               const int dst = cb * (C::TILE * 128) + b * p.box * (kStageHalf / C::TILE / CB);
-              tma_load_4d(kd + dst, &mk, full + st, cb * COLS, off, kvh, page);
-              tma_load_4d(kd + kStageHalf + dst, &mv, full + st, cb * COLS, off, kvh, page);
+              tma_load_4d(kd + dst, &mk, full + st, cb * COLS, axis(0), axis(1), axis(2));
+              tma_load_4d(kd + kStageHalf + dst, &mv, full + st, cb * COLS, axis(0), axis(1), axis(2));
             }
           }
           if (tile + 1 < t1) lookup(tile + 1, lane, npage, noff);
@@ -1204,14 +1205,20 @@ bool short_table(int D, bool bf, int64_t table_tokens) {
   return table_tokens <= (int64_t)kAlignTiles * (kStageHalf / (D * (bf ? 2 : 4)));
 }
 
-// A 4-D map over the cache, {D, slot, head, page}, box {cols, box, 1, 1}.
+// A 4-D map over the cache: D, then slot, head and page by increasing stride (each stride has to
+// be a multiple of the one before); boxes of `box` slots and `cols` elements.
 bool cache_map(CUtensorMap* map, const void* base, const PagedAttnArgs& a, int cols, int box) {
   EncodeTiledFn enc = tmap_encoder();
   if (enc == nullptr) return false;
   const int es = a.in_bf16 ? 2 : 4;
-  cuuint64_t dims[4] = {(cuuint64_t)a.D, (cuuint64_t)a.c.page_size, (cuuint64_t)a.Nkv, (cuuint64_t)a.c.num_pages};
-  cuuint64_t strides[3] = {(cuuint64_t)a.c.ss * es, (cuuint64_t)a.c.hs * es, (cuuint64_t)a.c.ps * es};
-  cuuint32_t bx[4] = {(cuuint32_t)cols, (cuuint32_t)box, 1, 1};
+  const int ext[3] = {a.c.page_size, a.Nkv, a.c.num_pages};
+  cuuint64_t dims[4] = {(cuuint64_t)a.D}, strides[3];
+  cuuint32_t bx[4] = {(cuuint32_t)cols};
+  for (int i = 0; i < 3; ++i) {
+    dims[i + 1] = (cuuint64_t)ext[a.c.order[i]];
+    strides[i] = (cuuint64_t)a.c.sorted[i] * es;
+    bx[i + 1] = a.c.order[i] == 0 ? (cuuint32_t)box : 1;
+  }
   cuuint32_t one[4] = {1, 1, 1, 1};
   return enc(map, a.in_bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4,
              const_cast<void*>(base), dims, strides, bx, one, CU_TENSOR_MAP_INTERLEAVE_NONE,

@@ -621,6 +621,8 @@ def attention_decode(q, k, v, k_cache, v_cache, block_table, kv_lens, cos_sin=No
     and k normed and rotated) -> paged_attn_decode (with the output gate).
 
     ``bufs`` (optional dict) supplies preallocated q, o, workspace."""
+    if gate is not None and (gate.dtype is not k_cache.dtype or gate.shape != q.shape):
+        raise ValueError('gate has the dtype of the cache and the shape of q')   # before the cache changes
     bufs = bufs or {}
     qr = paged_kv_append(k, v, k_cache, v_cache, block_table, kv_lens, q, cos_sin, q_norm_w, k_norm_w, positions,
                          cu_seqlens, norm_eps, interleaved, k_cache.dtype, bufs.get('q'))

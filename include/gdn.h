@@ -424,10 +424,12 @@ typedef struct {
 
 /* A paged key/value cache.  Element i of slot j of key/value head h in page p
  * is at p * page_stride + h * head_stride + j * slot_stride + i of k and of v
- * (strides in elements, positive multiples of 16 bytes, below 2^40 bytes;
- * slot_stride >= D), so both a [pages, Nkv, page_size, D] and a
- * [pages, page_size, Nkv, D] cache, or the two halves of a
- * [pages, 2, ...] one, can be passed.
+ * (strides in elements, positive multiples of 16 bytes, below 2^40 bytes), so
+ * both a [pages, Nkv, page_size, D] and a [pages, page_size, Nkv, D] cache, or
+ * the two halves of a [pages, 2, ...] one, can be passed.  In order of size,
+ * the strides of the axes with more than one entry are at least D and what the
+ * axis below spans (no two entries overlap), and each is a multiple of the one
+ * below (else GDN_ERR_UNSUPPORTED).
  *   block_table  [N, max_pages] int32: index p of sequence s lives in slot
  *                p % page_size of page block_table[s, p / page_size]; entries
  *                past a sequence's length are not read

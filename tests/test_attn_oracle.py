@@ -121,7 +121,9 @@ BOTH = [(dict(Nq=9), 'INVALID', 'multiple'), (dict(N=0), 'INVALID', 'num_seqs'),
 CACHE = [(dict(cache=False), 'INVALID', 'cache'), (dict(k=None), 'INVALID', 'cache_k'), (dict(v=X + 2), 'INVALID', 'cache_v'),
          (dict(bt=None), 'INVALID', 'block_table'), (dict(lens=X + 4), 'INVALID', 'kv_lens'),
          (dict(pages=0), 'INVALID', 'num_pages'), (dict(psize=0), 'INVALID', 'page_size'), (dict(maxp=0), 'INVALID', 'max_pages'),
-         (dict(ps=4095), 'INVALID', 'strides'), (dict(chs=0), 'INVALID', 'strides'), (dict(ss=120), 'INVALID', 'slot_stride'),
+         (dict(ps=4095), 'INVALID', 'strides'), (dict(chs=0), 'INVALID', 'strides'), (dict(ss=120), 'INVALID', 'overlap'),
+         (dict(chs=15 * 128), 'INVALID', 'overlap'), (dict(ps=16 * 128), 'INVALID', 'overlap'), (dict(ss=2 * 128, chs=64), 'INVALID', 'overlap'),
+         (dict(ps=2 * 16 * 128 + 8), 'UNSUPPORTED', 'multiples'), (dict(psize=1 << 30, ps=1 << 38, pages=1 << 30), 'INVALID', 'overlap'),
          (dict(ps=1 << 39), 'INVALID', 'strides')]
 NR = [(dict(rot=144), 'INVALID', 'rotary_dim'), (dict(rot=24), 'UNSUPPORTED', 'multiple of 16'),
       (dict(tab=None), 'INVALID', 'cos_sin'), (dict(maxpos=0), 'INVALID', 'max_positions'),

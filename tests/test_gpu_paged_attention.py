@@ -554,3 +554,75 @@ def test_long_contexts_back_to_back(D, H, dtype):
 
 def run_attn_async(c, q, n, dtype):
     return gdn.paged_attn_decode(q, c.k, c.v, c.block_table, i32([n]), out_dtype=dtype)
+
+
+def test_padded_strides():
+    """Slots and heads apart by more than they hold, in both orders; what lies between is left as it was."""
+    for order in ((0, 1, 2, 3), (0, 2, 1, 3)):                       # [page, head, slot, D] or [page, slot, head, D]
+        H, P, D, lens = 2, 16, 64, [40, 17]
+        c = Cache(lens, H, P, D, BF)
+        shape = [c.pages, H, P, D]
+        dims = [shape[i] for i in order]
+        views = []
+        for _ in range(2):
+            raw = torch.full((dims[0], dims[1] + 1, dims[2] + 1, D + 8), float('nan'), dtype=BF, device='cuda')
+            views.append((raw, raw[:, :dims[1], :dims[2], :D].permute(*order)))
+        (kr, c.k), (vr, c.v) = views
+        k, v, q = rand(1, 57, H, D), rand(2, 57, H, D), rand(3, 57, 8, D)
+        gdn.paged_kv_append(k, v, c.k, c.v, c.block_table, i32(lens), cu_seqlens=i32([0, 40, 57]))
+        check_attn(c, q, lens, lens)
+        for raw, x in ((kr, k), (vr, v)):
+            assert int((~raw.isnan()).sum()) == x.numel()
+
+
+def test_nothing_to_attend_at_all():
+    for n, width in ((1, 2), (5, 100)):
+        c = Cache([width * 16] * n, 2, 16, 128, BF)
+        o = torch.full((2 * n, 8, 128), 7.0, dtype=BF, device='cuda')
+        gdn.paged_attn_decode(rand(1, 2 * n, 8, 128), c.k, c.v, c.block_table, i32([0] * n), o=o)
+        gdn.check_device_error()
+        assert not o.any()
+
+
+def test_fewer_cached_than_new_and_negative_lengths():
+    for dtype in (BF, F32):
+        lens = [20, 20, 20]
+        q = rand(81, 6, 4, 64, dtype=dtype)
+        c = Cache(lens, 2, 16, 64, dtype).fill(lens, 82)
+        y = run_attn(c, q, lens, [2] * 3, out_dtype=dtype)
+        for bad in (1, -5):
+            z = gdn.paged_attn_decode(q, c.k, c.v, c.block_table, i32([20, bad, 20]), out_dtype=dtype)
+            with pytest.raises(RuntimeError, match='device error 3'):
+                gdn.check_device_error()
+            assert torch.equal(z[:2], y[:2]) and torch.equal(z[4:], y[4:]) and not z[2:4].any()
+
+
+def test_no_tokens():
+    c = Cache([16], 2, 16, 64, BF)
+    e = torch.empty(0, 4, 64, dtype=BF, device='cuda')
+    assert gdn.paged_attn_decode(e, c.k, c.v, c.block_table, i32([3])).shape == e.shape
+    assert gdn.qk_norm_rope(e, e[:, :2])[0].shape == e.shape
+    assert gdn.paged_kv_append(e[:, :2], e[:, :2], c.k, c.v, c.block_table, i32([3])) is None
+    gdn.check_device_error()
+    assert c.k.isnan().all()
+
+
+def test_a_gate_of_another_type_is_refused_before_the_cache_changes():
+    c = Cache([16], 2, 16, 64, BF)
+    q, k = rand(1, 1, 4, 64, dtype=F32), rand(2, 1, 2, 64, dtype=F32)
+    with pytest.raises(ValueError, match='gate'):
+        gdn.attention_decode(q, k, k, c.k, c.v, c.block_table, i32([3]), gate=q)
+    assert c.k.isnan().all()
+
+
+@pytest.mark.parametrize('N', [161, 1000, 5000])
+def test_more_sequences_than_threads(N):
+    """Every sequence of a large batch of one-token rows returns its only value."""
+    lens = [1 if s % 3 else 0 for s in range(N)]
+    c = Cache([1] * N, 1, 8, 64, BF)
+    v = rand(7, N, 1, 64)
+    gdn.paged_kv_append(v, v, c.k, c.v, c.block_table, i32(lens))
+    y = gdn.paged_attn_decode(rand(8, N, 2, 64), c.k, c.v, c.block_table, i32(lens))
+    gdn.check_device_error()
+    live = torch.tensor(lens, device='cuda').bool()
+    assert torch.equal(y[live], v[live].expand(-1, 2, -1)) and not y[~live].any()
