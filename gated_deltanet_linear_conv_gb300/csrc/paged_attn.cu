@@ -21,9 +21,8 @@
 // ranges end at unit borders instead and no second kernel runs.
 //
 // Inside a CTA a producer warp walks the range: it looks the page ids up and issues TMA
-// boxes of gcd(page size, tile) slots (so any page size tiles exactly; slots past the end
-// of a sequence come as the out-of-range zero fill) into a ring of stages, and the query
-// rows of each unit by bulk copies.  Four consumer warps take 16-token (bf16) or 4-token
+// boxes that end where pages do (slots past the end of a sequence come as the out-of-range
+// zero fill) into a ring of stages, and the query rows of each unit by bulk copies.  Four consumer warps take 16-token (bf16) or 4-token
 // (float32) slices with a maximum, sum and output of their own, joined through shared
 // memory once per unit.  With many rows (NT * D > 256) DS of them share a slice: each
 // computes the weights of NT / DS octets, they exchange them, and each accumulates D / DS
@@ -123,8 +122,9 @@ __host__ __device__ constexpr size_t align16(size_t x) { return (x + 15) & ~(siz
 struct Params {
   PagedAttnArgs a;
   int G, NG, rg_log;           // query heads per kv head, octets per token, log2 of the rows of an octet
-  Div by_NG, by_page;
-  int box, align;          // slots per TMA box; ranges end at unit borders
+  Div by_NG, by_page, by_tile;
+  int box, nbox, tile;     // slots per TMA box, boxes per tile, tokens per tile (<= C::TILE)
+  int align;               // ranges end at unit borders
   float c;                 // scale * log2(e)
   SplitRec* rec;           // [grid]
   float* part_o;           // [2 * grid][ROWS][D]
@@ -218,8 +218,7 @@ __device__ __forceinline__ Seq load_seq(const PagedAttnArgs& a, int s, int* err 
   if (!ok && err != nullptr) raise_error(err, kDevErrSeqlens);
   return {bos, n, n > 0 ? len : 0};
 }
-template <typename C>
-__device__ __forceinline__ int seq_tiles(const Seq& q) { return (q.len + C::TILE - 1) / C::TILE; }
+__device__ __forceinline__ int seq_tiles(const Params& p, const Seq& q) { return p.by_tile.quot(q.len + p.tile - 1); }
 template <typename C>
 __device__ __forceinline__ int seq_groups(const Params& p, const Seq& q) {   // octet groups per kv head
   return (int)(((int64_t)q.n * p.NG + C::NT - 1) / C::NT);
@@ -227,7 +226,7 @@ __device__ __forceinline__ int seq_groups(const Params& p, const Seq& q) {   // 
 
 template <typename C>
 __device__ __forceinline__ int64_t seq_work(const Params& p, const Seq& q) {
-  return q.len == 0 ? 0 : (int64_t)(seq_tiles<C>(q) + kUnitCost) * seq_groups<C>(p, q) * p.a.Nkv;
+  return q.len == 0 ? 0 : (int64_t)(seq_tiles(p, q) + kUnitCost) * seq_groups<C>(p, q) * p.a.Nkv;
 }
 
 // The next sequence behind s with anything to attend (the warp looks at 32 at a time); its
@@ -729,20 +728,19 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
     if (lo < hi) {
       int s = from_seq[0];
       Seq q{from_seq[1], from_seq[2], from_seq[3]};
-      int tiles = seq_tiles<C>(q), groups = seq_groups<C>(p, q);
+      int tiles = seq_tiles(p, q), groups = seq_groups<C>(p, q);
       int64_t seq_at = *from, pos = lo;
       int cost = tiles + kUnitCost;                // of a unit; its tiles lie at the end
       int unit = div_small(pos - seq_at, cost);
       if (p.align && seq_at + (int64_t)unit * cost < pos) ++unit;          // the first unit that starts here
       if (p.align) pos = seq_at + (int64_t)unit * cost;
-      const int nbox = C::TILE / p.box;
 #pragma unroll 1
       while (pos < hi) {
         if (unit >= groups * a.Nkv) {
           seq_at += (int64_t)cost * groups * a.Nkv;
           s = next_seq(a, s, &q);
           if (s >= a.num_seqs) break;              // (cannot be: pos < hi <= total)
-          tiles = seq_tiles<C>(q);
+          tiles = seq_tiles(p, q);
           groups = seq_groups<C>(p, q);
           cost = tiles + kUnitCost;
           unit = 0;
@@ -757,10 +755,10 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
         const int32_t* bt = a.c.bt + (int64_t)s * a.c.max_pages;
         // page and slot of this lane's first box, one tile ahead of its use
         auto lookup = [&](int tile, int b, int& page, int& off) {
-          const int tok = tile * C::TILE + b * p.box;
+          const int tok = tile * p.tile + b * p.box;
           page = a.c.num_pages;                    // out of range: zero fill
           off = 0;
-          if (tok < q.len && b < nbox) {
+          if (tok < q.len && b < p.nbox) {
             const int at = p.by_page.quot(tok);
             const int pg = __ldg(bt + at);
             off = tok - at * a.c.page_size;
@@ -777,10 +775,10 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
           ok = wait_bar(empty + st, ((it / C::STAGES) & 1) ^ 1, abort);
           if (!ok) break;
           uint8_t* kd = ring + st * 2 * kStageHalf;
-          if (lane == 0) tc::mbar_arrive_expect_tx(full + st, 2 * kStageHalf);
+          if (lane == 0) tc::mbar_arrive_expect_tx(full + st, p.tile * (2 * kStageHalf / C::TILE));
           __syncwarp();
 #pragma unroll 1
-          for (int b = lane; b < nbox; b += 32) {
+          for (int b = lane; b < p.nbox; b += 32) {
             if (b >= 32) lookup(tile, b, page, off);
             auto axis = [&](int i) { return a.c.order[i] == 0 ? off : a.c.order[i] == 1 ? kvh : page; };
 #pragma unroll
@@ -908,9 +906,10 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
       uint8_t* kd = ring + st * 2 * kStageHalf;
 #pragma unroll 1
       for (; j < C::SL; j += C::TG) {
-        const int tok0 = tile * C::TILE + j * C::SLICE;
-        if (tok0 < most) {
-          w.slice(kd, kd + kStageHalf, j * C::SLICE, tok0, d.nvalid, p.c, lim, tw, lane);
+        const int tok0 = tile * p.tile + j * C::SLICE, end = (tile + 1) * p.tile;
+        if (tok0 < min(most, end)) {
+          auto seen = [&](int nt) { return min(lim(nt), end); };           // rows behind the tile's last are not loaded
+          w.slice(kd, kd + kStageHalf, j * C::SLICE, tok0, d.nvalid, p.c, seen, tw, lane);
           any = true;
         }
       }
@@ -1200,6 +1199,21 @@ int octets_per_pass(int num_seqs, int total, int Nq, int Nkv, int D, bool bf) {
   return nt;
 }
 
+// Slots per box and boxes per tile: a box has to end where a page does.  Full tiles by the
+// greatest common divisor, unless that takes more than four boxes: one box costs about as much
+// as 1.5 KB of the stream, and with pages of 20 slots (eight boxes of 4 in a tile of 32) 16 x
+// 4096 tokens took 46 us against 29 with pages of 16.  Then tiles of the largest divisor of the
+// page, and a part of the tile empty.
+void tile_boxes(int page_size, int tile, int* box, int* n) {
+  *box = std::gcd(page_size, tile);
+  if (tile / *box > 4) {
+    int d = std::min(page_size, tile);
+    while (page_size % d != 0) --d;
+    *box = d;
+  }
+  *n = tile / *box;
+}
+
 // Tables so short that ranges end at unit borders.
 bool short_table(int D, bool bf, int64_t table_tokens) {
   return table_tokens <= (int64_t)kAlignTiles * (kStageHalf / (D * (bf ? 2 : 4)));
@@ -1247,7 +1261,9 @@ cudaError_t launch_c(const PagedAttnArgs& a, cudaStream_t s) {
   p.rg_log = RG == 8 ? 3 : 2;
   p.by_NG = Div::of(p.NG);
   p.by_page = Div::of(a.c.page_size);
-  p.box = std::gcd(a.c.page_size, C::TILE);
+  tile_boxes(a.c.page_size, C::TILE, &p.box, &p.nbox);
+  p.tile = p.box * p.nbox;
+  p.by_tile = Div::of(p.tile);
   p.align = short_table(D, C::BF, (int64_t)a.c.max_pages * a.c.page_size);
   p.c = a.scale * kLog2e;
   uint8_t* ws = static_cast<uint8_t*>(a.ws);
