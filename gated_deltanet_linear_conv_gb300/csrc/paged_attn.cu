@@ -1008,21 +1008,24 @@ __device__ __forceinline__ int64_t piece_row(int c0, int i, int rows, int row) {
   // CTA c0's last piece (slot 2 c0 + 1), then the first ones of the CTAs behind it
   return ((int64_t)2 * (c0 + i) + (i == 0 ? 1 : 0)) * rows + row;
 }
-// The nth CTA with a record, -1 if there are fewer (all threads of the block; PER * threads >= CTAs).
+// The record of the nth CTA that has one, and that CTA (-1 if there are fewer), for all threads of
+// the block: every record is loaded at once, so that finding the one costs no second load.
 template <int THREADS>
-__device__ __forceinline__ int nth_record(const Params& p, int ctas, int nth, int* found) {
+__device__ __forceinline__ SplitRec nth_record(const Params& p, int ctas, int nth, int* found, int& cta) {
   constexpr int PER = (kMaxCtas + THREADS - 1) / THREADS, WARPS = THREADS / 32;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  int valid[PER], cnt = 0;
+  SplitRec r[PER];
   uint32_t mask[PER];
+  int cnt = 0;
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
     const int c = (warp * PER + i) * 32 + lane;
-    valid[i] = c < ctas ? p.rec[c].valid : 0;
+    r[i].valid = 0;
+    if (c < ctas) r[i] = p.rec[c];
   }
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
-    mask[i] = __ballot_sync(0xffffffffu, valid[i] != 0);
+    mask[i] = __ballot_sync(0xffffffffu, r[i].valid != 0);
     cnt += __popc(mask[i]);
   }
   if (lane == 0) found[warp] = cnt;
@@ -1033,24 +1036,25 @@ __device__ __forceinline__ int nth_record(const Params& p, int ctas, int nth, in
   for (int i = 0; i < WARPS; ++i) at += i < warp ? found[i] : 0;
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
-    if (valid[i] != 0 && at + __popc(mask[i] & ((1u << lane) - 1)) == nth) found[WARPS] = (warp * PER + i) * 32 + lane;
+    if (r[i].valid != 0 && at + __popc(mask[i] & ((1u << lane) - 1)) == nth) {
+      found[WARPS] = (warp * PER + i) * 32 + lane;
+      *reinterpret_cast<SplitRec*>(found + WARPS + 1) = r[i];
+    }
     at += __popc(mask[i]);
   }
   __syncthreads();
-  return found[WARPS];
+  cta = found[WARPS];
+  return *reinterpret_cast<const SplitRec*>(found + WARPS + 1);
 }
 template <typename T, int D, int PG>
 __global__ void __launch_bounds__(kJoinThreads)
 paged_attn_join_kernel(const __grid_constant__ Params p, int ctas, int rows) {
-  __shared__ int found[kJoinThreads / 32 + 1];
+  __shared__ int found[kJoinThreads / 32 + 1 + sizeof(SplitRec) / 4];
   pdl_launch_next();
   pdl_wait();
   int c0 = blockIdx.x;
-  if (PG > 1) {
-    c0 = nth_record<kJoinThreads>(p, ctas, blockIdx.x, found);
-    if (c0 < 0) return;
-  }
-  const SplitRec r = p.rec[c0];
+  const SplitRec r = PG > 1 ? nth_record<kJoinThreads>(p, ctas, blockIdx.x, found, c0) : p.rec[c0];
+  if (c0 < 0) return;
   // lanes: 32 / PG column groups side by side, PG times
   const int lane = threadIdx.x & 31, k0 = lane / (32 / PG);
   const int i = (blockIdx.y * (kJoinThreads / 32) + (threadIdx.x >> 5)) * (32 / PG) + lane % (32 / PG);
@@ -1117,13 +1121,13 @@ paged_attn_join_few_kernel(const __grid_constant__ Params p, int ctas) {
   constexpr int WARPS = kFewThreads / 32;
   static_assert(kMaxCtas <= kFewThreads, "a thread per CTA");
   __shared__ float sw[kMaxCtas], so[WARPS][64], red[2][WARPS];
-  __shared__ int found[WARPS + 1];
+  __shared__ int found[WARPS + 1 + sizeof(SplitRec) / 4];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   pdl_launch_next();
   pdl_wait();
-  const int c0 = nth_record<kFewThreads>(p, ctas, blockIdx.x, found);
+  int c0;
+  const SplitRec r = nth_record<kFewThreads>(p, ctas, blockIdx.x, found, c0);
   if (c0 < 0) return;
-  const SplitRec r = p.rec[c0];
   const int row = blockIdx.y, oct = row >> p.rg_log, x = r.x0 + oct, t = p.by_NG.quot(x);
   const int h = ((x - t * p.NG - oct) << p.rg_log) + row;
   if (oct >= r.nvalid || h >= p.G) return;
