@@ -12,9 +12,10 @@
 // consecutive octets); its cache indices split into tiles of 8 KB of K and 8 KB of V.
 //
 // Work split.  All tiles of all units, laid end to end with a gap of kUnitCost for each
-// unit's start and join, are cut into one equal range per CTA (two CTAs per SM, one's starts and joins under the other's stream), from kv_lens as
-// they stand on the device: ragged batches and a single long context keep every SM equally
-// busy, and neither the host nor a captured graph needs the lengths.  A unit inside one
+// unit's start and join, are cut into one equal range per CTA (two CTAs per SM, one's starts
+// and joins under the other's stream), from kv_lens as they stand on the device: ragged
+// batches and a single long context keep every SM equally busy, and neither the host nor a
+// captured graph needs the lengths.  A unit inside one
 // range is finished by its CTA; the pieces of a unit that crosses ranges (at most one cut
 // per CTA) go to the workspace, unnormalised with their maxima and sums, and a second small
 // kernel joins them in order.  With short tables (no unit can exceed kAlignTiles tiles)
@@ -22,9 +23,9 @@
 //
 // Inside a CTA a producer warp walks the range: it looks the page ids up and issues TMA
 // boxes that end where pages do (slots past the end of a sequence come as the out-of-range
-// zero fill) into a ring of stages, and the query rows of each unit by bulk copies.  Four consumer warps take 16-token (bf16) or 4-token
-// (float32) slices with a maximum, sum and output of their own, joined through shared
-// memory once per unit.  With many rows (NT * D > 256) DS of them share a slice: each
+// zero fill) into a ring of stages, and the query rows of each unit by bulk copies.  Four
+// consumer warps take 16-token (bf16) or 4-token (float32) slices with a maximum, sum and
+// output of their own, joined through shared memory once per unit.  With many rows (NT * D > 256) DS of them share a slice: each
 // computes the weights of NT / DS octets, they exchange them, and each accumulates D / DS
 // columns of the output of all octets, so that a warp never holds more than 64 accumulators.
 
@@ -676,6 +677,11 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
     tc::prefetch_tmap(&mk);
     tc::prefetch_tmap(&mv);
   }
+  // rows of an octet without a query head are never copied: finite, or their columns would be
+  // rescaled at every slice
+#pragma unroll 1
+  for (int i = tid; i < C::QBYTES / 16; i += C::THREADS) reinterpret_cast<uint4*>(qs)[i] = make_uint4(0, 0, 0, 0);
+  tc::fence_proxy_async_smem();
   pdl_wait();
   // all tiles, and the sequence that this CTA's range starts in
   const int per = (a.num_seqs + C::THREADS - 1) / C::THREADS;
@@ -850,17 +856,15 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
       }
     }
     if (lane == 0 && !p.align) p.rec[blockIdx.x] = rec;
-    if (!ok) {
-      if (lane == 0) {
-        *abort = 1;
-        raise_error(a.err, kDevErrTimeout);
-      }
-      // copies in flight land before the CTA's shared memory goes
-      int none = 0;
-#pragma unroll 1
-      for (int i = max(0, it - C::STAGES); i < it; ++i) wait_bar(full + i % C::STAGES, (i / C::STAGES) & 1, &none);
-      if (npiece > 0) wait_bar(qfull, (npiece - 1) & 1, &none);
+    if (!ok && lane == 0) {
+      *abort = 1;
+      raise_error(a.err, kDevErrTimeout);
     }
+    // every copy lands before the CTA's shared memory goes, whatever the consumers do
+    int none = 0;
+#pragma unroll 1
+    for (int i = max(0, it - C::STAGES); i < it; ++i) wait_bar(full + i % C::STAGES, (i / C::STAGES) & 1, &none);
+    if (!ok && npiece > 0) wait_bar(qfull, (npiece - 1) & 1, &none);
     return;
   }
 

@@ -294,7 +294,8 @@ def test_attention_page_sizes(P, D, dtype):
     check_attn(c, q, LENS, [1] * len(LENS), gate, out_dtype=F32)
 
 
-@pytest.mark.parametrize('D,dtype,G', [(64, BF, 8), (128, BF, 4), (256, BF, 8), (256, BF, 16), (128, F32, 8), (64, F32, 3)])
+@pytest.mark.parametrize('D,dtype,G', [(64, BF, 8), (128, BF, 4), (256, BF, 8), (256, BF, 16), (128, F32, 8), (64, F32, 3), (64, F32, 8), (128, F32, 3), (256, F32, 4),
+                                       (256, F32, 6), (64, F32, 12)])
 def test_attention_several_new_tokens(D, dtype, G):
     """Draft + verify with ragged counts, an inactive slot, no tokens, and a whole prompt at once."""
     new, lens = [1, 4, 0, 3, 2, 37, 8], [50, 4, 30, 66, 0, 37, 300]
@@ -303,7 +304,7 @@ def test_attention_several_new_tokens(D, dtype, G):
     check_attn(c, q, lens, new, gate, out_dtype=dtype)
 
 
-@pytest.mark.parametrize('D,dtype', [(64, BF), (128, BF), (256, BF), (128, F32), (256, F32)])
+@pytest.mark.parametrize('D,dtype', [(64, BF), (128, BF), (256, BF), (64, F32), (128, F32), (256, F32)])
 def test_later_tokens_never_reach_a_row(D, dtype):
     """NaN and infinities in a later new token's key and value leave the earlier rows as they are."""
     new, lens = [4, 3], [77, 35]
