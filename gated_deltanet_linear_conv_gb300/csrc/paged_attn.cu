@@ -3,9 +3,10 @@
 //   o[t, h] = sum_j softmax_j(scale q[t, h] . k_j) v_j, then * sigmoid(gate[t, h]).
 //
 // Bound: every visible key and value is read once per call and used by the G = Nq / Nkv
-// query heads of its head, 2 G flops per byte in bf16 (G / 2 per byte pair in float32): far
-// below the matrix ridge, so the kernel is a stream of the cache at HBM rate with the
-// softmax riding along (one pass, running maximum and sum).
+// query heads of its head, 2 G flops per byte in bf16 and G in float32 for each new token:
+// in bf16 far below the matrix ridge, so the kernel is a stream of the cache at HBM rate with
+// the softmax riding along (one pass, running maximum and sum).  float32 is that for one
+// token; with more, the CUDA cores bound it.
 //
 // Rows.  The 8 columns of a product tile (an octet) are query heads of one token and one
 // kv head; all its columns see the same cache indices.  A unit is (sequence, kv head, NT
@@ -25,9 +26,10 @@
 // boxes that end where pages do (slots past the end of a sequence come as the out-of-range
 // zero fill) into a ring of stages, and the query rows of each unit by bulk copies.  Four
 // consumer warps take 16-token (bf16) or 4-token (float32) slices with a maximum, sum and
-// output of their own, joined through shared memory once per unit.  With many rows (NT * D > 256) DS of them share a slice: each
-// computes the weights of NT / DS octets, they exchange them, and each accumulates D / DS
-// columns of the output of all octets, so that a warp never holds more than 64 accumulators.
+// output of their own, joined through shared memory once per unit.  With many rows in bf16
+// (NT * D > 256) DS of them share a slice: each computes the weights of NT / DS octets, they
+// exchange them, and each accumulates D / DS columns of the output of all octets, so that a
+// warp never holds more than 64 accumulators.
 
 #include <numeric>
 
@@ -430,7 +432,8 @@ struct TcWarp {
       ldsm4t(vbase + (i >> 2) * (C::TILE * 128) + ((ch ^ vsw) << 4), a);
     };
     // Rows that an octet does not see may hold anything, and 0 * NaN is NaN: at the end of the
-    // visible range they are cleared in the stage, in the columns that this warp reads.
+    // visible range they are cleared in the stage, in the columns that this warp reads, once
+    // where all octets see the same (mixed: the slice holds new tokens that only some see).
     auto clear = [&](int last) {
 #pragma unroll 1
       for (int e = lane; e < (16 - last) * (2 * OS); e += 32) {
@@ -439,7 +442,8 @@ struct TcWarp {
       }
       __syncwarp();
     };
-    if (NT > 1 && tail) {
+    const bool mixed = tail && min(lim(NT - 1), tok0 + 16) > lim(0);
+    if (NT > 1 && mixed) {
       // from the octet that sees most to the one that sees least
 #pragma unroll
       for (int nt = NT - 1; nt >= 0; --nt) {
@@ -455,7 +459,7 @@ struct TcWarp {
         __syncwarp();
       }
     } else {
-      if (tail) clear(min(16, lim(0) - tok0));
+      if (tail) clear(max(0, min(16, lim(0) - tok0)));
 #pragma unroll
       for (int i = 0; i < OS; ++i) {
         uint32_t a[4];
@@ -496,23 +500,28 @@ struct TcWarp {
 };
 
 // float32 on the CUDA cores, four tokens at a time.  Eight lanes span a head row; the four
-// groups of eight take two heads each (or one, where the kv head has at most four), so that
+// groups of eight take two rows of an octet each (or one, where an octet has four), so that
 // a dot product is summed over 8 lanes only: with 32 lanes across the row the exchanges were
-// half of the instructions (147 per token and warp, 54 % of the issue slots).  The sums end
-// with one score of the 8 x 4 per lane: one exponential each.  Element pairs go through the
-// packed fp32x2 operations.
-template <int D, int RG>
+// half of the instructions (147 per token and warp, 54 % of the issue slots), with 4 the reads
+// of shared memory bound it.  The sums end with one score of the 8 x 4 per lane and octet: one
+// exponential each.  NT octets share what is read of the cache; their reductions run side by
+// side, without a branch between them.  6 new tokens of 149 sequences of 6511 (64-wide heads, 8
+// per kv head, pages of 20) took 995 us with one octet at a time, 886 with four, 591 with the two
+// whose queries and outputs stay in registers.  Element pairs go through the packed fp32x2
+// operations.  (Products in three tf32 parts on the matrix
+// instructions were slower but for 64-wide heads: the splits cost more than they save.)
+template <int D, int NT, int RG>
 struct SimtWarp {
-  using C = Cfg<float, D, 1, RG>;
+  using C = Cfg<float, D, NT, RG>;
   static constexpr int E = D / 32;                 // 4-element chunks per lane: columns 32 i + 4 (lane % 8)
-  static constexpr int H = RG / 4;                 // heads per lane group
-  static constexpr bool QREG = H * E < 16;         // queries in registers; at 64 of them they stay in shared memory
-  float2 q[QREG ? H : 1][QREG ? E : 1][2], o[H][E][2];
+  static constexpr int H = RG / 4;                 // rows of an octet per lane group
+  static constexpr bool QREG = NT * H * E < 16;    // queries in registers; at 64 of them they stay in shared memory
+  float2 q[QREG ? NT : 1][QREG ? H : 1][QREG ? E : 1][2], o[NT][H][E][2];
+  float m[NT], l[NT];                              // of row `mine`
   uint32_t q_at;
-  float m, l;                                      // of head `mine`
 
   static __device__ __forceinline__ int mine(int lane) { return RG == 8 ? lane >> 2 : lane >> 3; }
-  // lane that holds the score of this lane group's head h, token i
+  // lane that holds the score of this lane group's row h, token i
   static __device__ __forceinline__ int holder(int lane, int h, int i) { return (lane & 24) + h * 4 + i; }
   static __device__ __forceinline__ void chunk(uint32_t at, float2 (&x)[2]) {
     asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(x[0].x), "=f"(x[0].y), "=f"(x[1].x), "=f"(x[1].y)
@@ -521,119 +530,145 @@ struct SimtWarp {
   __device__ __forceinline__ void start(const uint8_t* qs, int, uint8_t*, int lane) {
     q_at = tc::smem_u32(qs) + (lane >> 3) * H * C::QPITCH + (lane & 7) * 16;
 #pragma unroll
-    for (int h = 0; h < H; ++h)
+    for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-      for (int e = 0; e < E; ++e) {
-        if (QREG) chunk(q_at + h * C::QPITCH + e * 128, q[h][e]);
-        o[h][e][0] = o[h][e][1] = make_float2(0.f, 0.f);
-      }
-    m = -INFINITY;
-    l = 0.f;
+      for (int h = 0; h < H; ++h)
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          if (QREG) chunk(q_at + (nt * RG + h) * C::QPITCH + e * 128, q[nt][h][e]);
+          o[nt][h][e][0] = o[nt][h][e][1] = make_float2(0.f, 0.f);
+        }
+      m[nt] = -INFINITY;
+      l[nt] = 0.f;
+    }
   }
   template <typename Lim>
   __device__ __forceinline__ void slice(uint8_t* ks_, uint8_t* vs_, int j0, int tok0, int, float c, Lim lim,
                                         int, int lane) {
-    const int last = lim(0) - tok0;                // tokens of the slice that are visible (> 0)
     const uint32_t k_at = tc::smem_u32(ks_) + j0 * (D * 4) + (lane & 7) * 16;
     const uint32_t v_at = tc::smem_u32(vs_) + j0 * (D * 4) + (lane & 7) * 16;
-    float2 a[4][H];
+    float2 a[4][NT][H];
 #pragma unroll
     for (int e = 0; e < E; ++e) {
-      float2 qe[H][2];
+      float2 k[4][2];
 #pragma unroll
-      for (int h = 0; h < H; ++h) {
-        if (QREG) {
-          qe[h][0] = q[h][e][0];
-          qe[h][1] = q[h][e][1];
-        } else {
-          chunk(q_at + h * C::QPITCH + e * 128, qe[h]);
-        }
-      }
+      for (int i = 0; i < 4; ++i) chunk(k_at + i * (D * 4) + e * 128, k[i]);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        float2 k[2];
-        chunk(k_at + i * (D * 4) + e * 128, k);
+      for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
         for (int h = 0; h < H; ++h) {
-          a[i][h] = e == 0 ? __fmul2_rn(qe[h][0], k[0]) : __ffma2_rn(qe[h][0], k[0], a[i][h]);
-          a[i][h] = __ffma2_rn(qe[h][1], k[1], a[i][h]);
+          float2 qe[2];
+          if (QREG) {
+            qe[0] = q[nt][h][e][0];
+            qe[1] = q[nt][h][e][1];
+          } else {
+            chunk(q_at + (nt * RG + h) * C::QPITCH + e * 128, qe);
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            a[i][nt][h] = e == 0 ? __fmul2_rn(qe[0], k[i][0]) : __ffma2_rn(qe[0], k[i][0], a[i][nt][h]);
+            a[i][nt][h] = __ffma2_rn(qe[1], k[i][1], a[i][nt][h]);
+          }
         }
       }
     }
-    float s = 0.f;
+    // step by step for all octets, without a branch between them: each step's exchanges overlap
+    float p[NT], al[NT];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      float d;
-      if (H == 2) {                                // lanes 4..7 of a group go on with the second head
-        const bool up = (lane & 4) != 0;
-        const float d0 = a[i][0].x + a[i][0].y, d1 = a[i][H - 1].x + a[i][H - 1].y;
-        d = (up ? d1 : d0) + __shfl_xor_sync(0xffffffffu, up ? d0 : d1, 4);
-      } else {
-        d = a[i][0].x + a[i][0].y;
-        d += __shfl_xor_sync(0xffffffffu, d, 4);
-      }
-      d += __shfl_xor_sync(0xffffffffu, d, 2);
-      d += __shfl_xor_sync(0xffffffffu, d, 1);
-      if ((lane & 3) == i) s = d;
-    }
-    s = (lane & 3) < last ? s * c : -INFINITY;
-    float mx = fmaxf(s, __shfl_xor_sync(0xffffffffu, s, 1));
-    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-    if (__any_sync(0xffffffffu, mx > m)) {
-      const float mn = fmaxf(m, mx);
-      const float al = mn == m ? 1.f : ex2(m - mn);
-      m = mn;
-      l *= al;
+    for (int nt = 0; nt < NT; ++nt) {
+      p[nt] = 0.f;
 #pragma unroll
-      for (int h = 0; h < H; ++h) {
-        const float a = __shfl_sync(0xffffffffu, al, holder(lane, h, 0));
-#pragma unroll
-        for (int e = 0; e < E; ++e)
-#pragma unroll
-          for (int f = 0; f < 2; ++f) o[h][e][f] = __fmul2_rn(o[h][e][f], make_float2(a, a));
+      for (int i = 0; i < 4; ++i) {
+        float d;
+        if (H == 2) {                              // lanes 4..7 of a group go on with the second row
+          const bool up = (lane & 4) != 0;
+          const float d0 = a[i][nt][0].x + a[i][nt][0].y, d1 = a[i][nt][H - 1].x + a[i][nt][H - 1].y;
+          d = (up ? d1 : d0) + __shfl_xor_sync(0xffffffffu, up ? d0 : d1, 4);
+        } else {
+          d = a[i][nt][0].x + a[i][nt][0].y;
+          d += __shfl_xor_sync(0xffffffffu, d, 4);
+        }
+        d += __shfl_xor_sync(0xffffffffu, d, 2);
+        d += __shfl_xor_sync(0xffffffffu, d, 1);
+        if ((lane & 3) == i) p[nt] = d;
       }
     }
-    const float p = ex2(s - (m == -INFINITY ? 0.f : m));
-    l += p;
-    float w[4][H];                                 // 0 for rows that may hold anything: those are not read into o
+    int last[NT];                                  // tokens of the slice that an octet sees (not falling with nt)
+    bool up = false;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int nt = 0; nt < NT; ++nt) {
+      last[nt] = lim(nt) - tok0;
+      p[nt] = (lane & 3) < last[nt] ? p[nt] * c : -INFINITY;
+      float mx = fmaxf(p[nt], __shfl_xor_sync(0xffffffffu, p[nt], 1));
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+      const float mn = fmaxf(m[nt], mx);
+      al[nt] = mn == m[nt] ? 1.f : ex2(m[nt] - mn);
+      up = up || al[nt] != 1.f;
+      m[nt] = mn;
+      p[nt] = ex2(p[nt] - (mn == -INFINITY ? 0.f : mn));
+      l[nt] = fmaf(l[nt], al[nt], p[nt]);
+    }
+    if (__any_sync(0xffffffffu, up)) {
 #pragma unroll
-      for (int h = 0; h < H; ++h) w[i][h] = __shfl_sync(0xffffffffu, p, holder(lane, h, i));
+      for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if (i < last) {
+        for (int h = 0; h < H; ++h) {
+          const float f = __shfl_sync(0xffffffffu, al[nt], holder(lane, h, 0));
 #pragma unroll
-        for (int e = 0; e < E; ++e) {
-          float2 v[2];
-          chunk(v_at + i * (D * 4) + e * 128, v);
+          for (int e = 0; e < E; ++e)
 #pragma unroll
-          for (int h = 0; h < H; ++h)
+            for (int k = 0; k < 2; ++k) o[nt][h][e][k] = __fmul2_rn(o[nt][h][e][k], make_float2(f, f));
+        }
+    }
+    auto values = [&](int i, bool all) {           // a token's values into the octets that see it
+      float2 v[E][2];
 #pragma unroll
-            for (int f = 0; f < 2; ++f) o[h][e][f] = __ffma2_rn(make_float2(w[i][h], w[i][h]), v[f], o[h][e][f]);
+      for (int e = 0; e < E; ++e) chunk(v_at + i * (D * 4) + e * 128, v[e]);
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        if (!all && i >= last[nt]) continue;       // what an octet does not see may hold anything
+#pragma unroll
+        for (int h = 0; h < H; ++h) {
+          const float x = __shfl_sync(0xffffffffu, p[nt], holder(lane, h, i));
+#pragma unroll
+          for (int e = 0; e < E; ++e)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) o[nt][h][e][k] = __ffma2_rn(make_float2(x, x), v[e][k], o[nt][h][e][k]);
         }
       }
+    };
+    if (last[0] >= 4) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) values(i, true);
+    } else {
+#pragma unroll 1
+      for (int i = 0; i < min(4, last[NT - 1]); ++i) values(i, false);
     }
   }
   __device__ __forceinline__ void give(float* jo, float* jm, float* jl, bool any, int lane) {
-    float v = l;
-    v += __shfl_xor_sync(0xffffffffu, v, 1);
-    v += __shfl_xor_sync(0xffffffffu, v, 2);
-    if ((lane & 3) == 0 && (RG == 8 || (lane & 4) == 0)) {
-      jm[mine(lane)] = m;
-      jl[mine(lane)] = v;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      float v = l[nt];
+      v += __shfl_xor_sync(0xffffffffu, v, 1);
+      v += __shfl_xor_sync(0xffffffffu, v, 2);
+      if ((lane & 3) == 0 && (RG == 8 || (lane & 4) == 0)) {
+        jm[nt * RG + mine(lane)] = m[nt];
+        jl[nt * RG + mine(lane)] = v;
+      }
     }
     if (!any) return;
 #pragma unroll
-    for (int h = 0; h < H; ++h)
+    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int e = 0; e < E; ++e)
-        *reinterpret_cast<float4*>(jo + ((lane >> 3) * H + h) * C::JP + e * 32 + (lane & 7) * 4) =
-            make_float4(o[h][e][0].x, o[h][e][0].y, o[h][e][1].x, o[h][e][1].y);
+      for (int h = 0; h < H; ++h)
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+          *reinterpret_cast<float4*>(jo + (nt * RG + (lane >> 3) * H + h) * C::JP + e * 32 + (lane & 7) * 4) =
+              make_float4(o[nt][h][e][0].x, o[nt][h][e][0].y, o[nt][h][e][1].x, o[nt][h][e][1].y);
   }
 };
 template <typename T, int D, int NT, int RG> struct WarpOf { using type = TcWarp<D, NT>; };
-template <int D, int NT, int RG> struct WarpOf<float, D, NT, RG> { using type = SimtWarp<D, RG>; };
+template <int D, int NT, int RG> struct WarpOf<float, D, NT, RG> { using type = SimtWarp<D, NT, RG>; };
 
 // ------------------------------------------------------------------ the main kernel
 template <typename T, int D, int NT, int RG>
@@ -876,6 +911,11 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
     if (q.n > 0 && q.len == 0) zero_rows(a, q);
   }
   const int tw = warp % C::TG;                     // which slices; warps tw + k TG share them
+  // The slices go round the warps from stage to stage.  In float32 also where tiles are not full:
+  // with pages of 20 slots five slices of four tokens on four warps took 592 us for the case at
+  // SimtWarp, this way 461.  In bf16 the arithmetic is not what bounds such tiles, and a count
+  // that is no constant cost full ones (45.0 against 47.5 us for 35 ragged sequences, 64-wide heads).
+  const int turn = C::BF || C::SL < C::TG ? C::SL : (p.tile + C::SLICE - 1) / C::SLICE;
   typename WarpOf<T, D, NT, RG>::type w;
   int it = 0;
   // After a wait that ran out a warp carries on with what the stages hold until the next
@@ -900,8 +940,8 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
     bool any = false;
 #pragma unroll 1
     for (int tile = d.tile0; tile < d.tile1; ++tile, ++it) {
-      int j = C::SL >= C::TG ? tw : tw - (it * C::SL) % C::TG;             // this warp's first slice of the stage
-      if (j < 0 || j >= C::SL) continue;
+      int j = (tw - it * turn) & (C::TG - 1);      // this warp's first slice of the stage
+      if (j >= C::SL) continue;
       const int st = it % C::STAGES;
       if (!wait_bar(full + st, (it / C::STAGES) & 1, abort)) {
         ok = false;
@@ -1197,13 +1237,21 @@ paged_attn_join_few_kernel(const __grid_constant__ Params p, int ctas) {
 }
 
 // ------------------------------------------------------------------ host
+// Rows of an octet: in float32 four where the kv head has no more heads, half the arithmetic
+// of eight (with more heads, eight rows mean fewer octets).
+int octet_rows(int Nq, int Nkv, bool bf) { return !bf && Nq / Nkv <= 4 ? 4 : 8; }
+
 // Octets per pass: enough for the new tokens of an even batch (a unit's rows then read
-// the cache once), up to the four whose outputs fit the registers.
+// the cache once), up to as many as the registers hold the outputs of.  In float32 a
+// pass of four takes 1.7 times one of two (16 x 4096 tokens, 128-wide heads: 87 and 50 us), so
+// twos where the last four would be half empty (153 sequences with 6 octets: 46 against 55 us).
 int octets_per_pass(int num_seqs, int total, int Nq, int Nkv, int D, bool bf) {
-  if (!bf) return 1;
-  const int64_t want = (int64_t)((total + num_seqs - 1) / num_seqs) * ((Nq / Nkv + 7) / 8);
+  const int rg = octet_rows(Nq, Nkv, bf);
+  const int64_t want = (int64_t)((total + num_seqs - 1) / num_seqs) * ((Nq / Nkv + rg - 1) / rg);
+  const int most = bf ? 4 : std::min(rg == 8 ? 2 : 4, 2048 / (D * rg));
   int nt = 1;
-  while (nt < want && nt < 4) nt *= 2;
+  while (nt < want && nt < most) nt *= 2;
+  if (!bf && nt == 4 && want > 4 && (want - 1) % 4 < 2) nt = 2;
   return nt;
 }
 
@@ -1308,11 +1356,15 @@ cudaError_t launch_bf16(const PagedAttnArgs& a, int nt, cudaStream_t s) {
   return launch_c<bf16, D, 4>(a, s);
 }
 
-// Four rows where the kv head has no more: half the arithmetic of eight.  (With more heads
-// than four, eight rows mean fewer passes over the cache.)
-template <int D>
-cudaError_t launch_f32(const PagedAttnArgs& a, cudaStream_t s) {
-  return a.Nq / a.Nkv <= 4 ? launch_c<float, D, 1, 4>(a, s) : launch_c<float, D, 1, 8>(a, s);
+template <int D, int RG>
+cudaError_t launch_f32(const PagedAttnArgs& a, int nt, cudaStream_t s) {
+  if constexpr (RG == 4 && D <= 128) {
+    if (nt == 4) return launch_c<float, D, 4, RG>(a, s);
+  }
+  if constexpr (D * RG <= 1024) {
+    if (nt == 2) return launch_c<float, D, 2, RG>(a, s);
+  }
+  return nt == 1 ? launch_c<float, D, 1, RG>(a, s) : cudaErrorInvalidValue;
 }
 
 }  // namespace
@@ -1328,7 +1380,9 @@ cudaError_t launch_paged_attn(const PagedAttnArgs& a, cudaStream_t s) {
   const int nt = octets_per_pass(a.num_seqs, a.total, a.Nq, a.Nkv, a.D, a.in_bf16);
   if (a.in_bf16)
     return a.D == 64 ? launch_bf16<64>(a, nt, s) : a.D == 128 ? launch_bf16<128>(a, nt, s) : launch_bf16<256>(a, nt, s);
-  return a.D == 64 ? launch_f32<64>(a, s) : a.D == 128 ? launch_f32<128>(a, s) : launch_f32<256>(a, s);
+  if (octet_rows(a.Nq, a.Nkv, false) == 4)
+    return a.D == 64 ? launch_f32<64, 4>(a, nt, s) : a.D == 128 ? launch_f32<128, 4>(a, nt, s) : launch_f32<256, 4>(a, nt, s);
+  return a.D == 64 ? launch_f32<64, 8>(a, nt, s) : a.D == 128 ? launch_f32<128, 8>(a, nt, s) : launch_f32<256, 8>(a, nt, s);
 }
 
 }  // namespace gdn
