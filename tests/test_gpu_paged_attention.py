@@ -304,6 +304,20 @@ def test_attention_several_new_tokens(D, dtype, G):
     check_attn(c, q, lens, new, gate, out_dtype=dtype)
 
 
+@pytest.mark.parametrize('P', [20, 12, 3])
+@pytest.mark.parametrize('D,G,n', [(64, 3, 4), (64, 8, 6), (128, 4, 4), (128, 4, 5), (128, 8, 2), (256, 4, 2), (256, 8, 3)])
+@pytest.mark.parametrize('dtype', [BF, F32])
+def test_several_new_tokens_in_tiles_that_are_not_full(P, D, G, n, dtype):
+    """Every count of octets per pass, with a last pass that is not full, over whole and cut units."""
+    lens = [n, 19, 20, 21, 61, 333, 1200]
+    c = Cache(lens, 1, P, D, dtype).fill(lens, 35)
+    q = rand(36, n * len(lens), G, D, dtype=dtype)
+    check_attn(c, q, lens, [n] * len(lens), out_dtype=dtype)
+    new = [n] * len(lens)
+    new[1], new[4] = n - 1, n + 1
+    check_attn(c, q, lens, new, out_dtype=dtype)
+
+
 @pytest.mark.parametrize('D,dtype', [(64, BF), (128, BF), (256, BF), (64, F32), (128, F32), (256, F32)])
 def test_later_tokens_never_reach_a_row(D, dtype):
     """NaN and infinities in a later new token's key and value leave the earlier rows as they are."""
