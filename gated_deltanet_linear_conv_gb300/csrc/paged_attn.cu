@@ -508,8 +508,10 @@ struct TcWarp {
 // side, without a branch between them.  6 new tokens of 149 sequences of 6511 (64-wide heads, 8
 // per kv head, pages of 20) took 995 us with one octet at a time, 886 with four, 591 with the two
 // whose queries and outputs stay in registers.  Element pairs go through the packed fp32x2
-// operations.  (Products in three tf32 parts on the matrix
-// instructions were slower but for 64-wide heads: the splits cost more than they save.)
+// operations.  Slower were products in three tf32 parts on the matrix instructions (but for
+// 64-wide heads: the splits cost more than they save) and a token per lane group with all rows in
+// each (a quarter of the shared memory reads, but longer chains: 34.8 against 30.8 us for 32
+// ragged sequences of up to 4000, 111 against 87 for 16 x 4096 with four new tokens each).
 template <int D, int NT, int RG>
 struct SimtWarp {
   using C = Cfg<float, D, NT, RG>;
