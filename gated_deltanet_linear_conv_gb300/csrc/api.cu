@@ -11,6 +11,7 @@
 
 #include "gdn.h"
 #include "launch.h"
+#include "paged_attn.h"
 
 namespace {
 

@@ -17,8 +17,8 @@
 //    whole and, in the half-split pairing, its partners are one other chunk);
 //  - addresses walk by the head stride; element pairs go through the packed fp32x2 operations.
 
-#include "common.cuh"
-#include "launch.h"
+#include "attn_util.cuh"
+#include "paged_attn.h"
 #include "tc_util.cuh"
 
 namespace gdn {

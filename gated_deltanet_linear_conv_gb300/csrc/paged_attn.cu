@@ -33,8 +33,8 @@
 
 #include <numeric>
 
-#include "common.cuh"
-#include "launch.h"
+#include "attn_util.cuh"
+#include "paged_attn.h"
 #include "tc_util.cuh"
 #include "tmap.cuh"
 
