@@ -1,4 +1,4 @@
-"""GB300 (sm_103a) Gated DeltaNet token mixer.
+"""GB300 (sm_103a) Gated DeltaNet token mixer, and decode attention over a paged cache.
 
 ``gdn`` binds the C-ABI CUDA library libgdn.so (built by ``build()``);
 ``inputs`` draws the seeded synthetic workloads.  The library is loaded on
