@@ -31,8 +31,6 @@
 // exchange them, and each accumulates D / DS columns of the output of all octets, so that a
 // warp never holds more than 64 accumulators.
 
-#include <numeric>
-
 #include "attn_util.cuh"
 #include "paged_attn.h"
 #include "tc_util.cuh"
@@ -507,7 +505,7 @@ struct TcWarp {
 // exponential each.  NT octets share what is read of the cache; their reductions run side by
 // side, without a branch between them.  6 new tokens of 149 sequences of 6511 (64-wide heads, 8
 // per kv head, pages of 20) took 995 us with one octet at a time, 886 with four, 591 with the two
-// whose queries and outputs stay in registers.  Element pairs go through the packed fp32x2
+// whose queries and outputs stay in registers (440 with what followed elsewhere).  Element pairs go through the packed fp32x2
 // operations.  Slower were products in three tf32 parts on the matrix instructions (but for
 // 64-wide heads: the splits cost more than they save) and a token per lane group with all rows in
 // each (a quarter of the shared memory reads, but longer chains: 34.8 against 30.8 us for 32
@@ -914,9 +912,9 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
   }
   const int tw = warp % C::TG;                     // which slices; warps tw + k TG share them
   // The slices go round the warps from stage to stage.  In float32 also where tiles are not full:
-  // with pages of 20 slots five slices of four tokens on four warps took 592 us for the case at
-  // SimtWarp, this way 461.  In bf16 the arithmetic is not what bounds such tiles, and a count
-  // that is no constant cost full ones (45.0 against 47.5 us for 35 ragged sequences, 64-wide heads).
+  // five slices of four tokens on four warps took 592 us for the case at SimtWarp (in tiles of
+  // 20), this way 461.  In bf16 the arithmetic is not what bounds such tiles, and a count that is
+  // no constant cost full ones (45.0 against 47.5 us for 35 ragged sequences, 64-wide heads).
   const int turn = C::BF || C::SL < C::TG ? C::SL : (p.tile + C::SLICE - 1) / C::SLICE;
   typename WarpOf<T, D, NT, RG>::type w;
   int it = 0;
@@ -1257,19 +1255,27 @@ int octets_per_pass(int num_seqs, int total, int Nq, int Nkv, int D, bool bf) {
   return nt;
 }
 
-// Slots per box and boxes per tile: a box has to end where a page does.  Full tiles by the
-// greatest common divisor, unless that takes more than four boxes: one box costs about as much
-// as 1.5 KB of the stream, and with pages of 20 slots (eight boxes of 4 in a tile of 32) 16 x
-// 4096 tokens took 46 us against 29 with pages of 16.  Then tiles of the largest divisor of the
-// page, and a part of the tile empty.
-void tile_boxes(int page_size, int tile, int* box, int* n) {
-  *box = std::gcd(page_size, tile);
-  if (tile / *box > 4) {
-    int d = std::min(page_size, tile);
-    while (page_size % d != 0) --d;
-    *box = d;
+// Slots per box and boxes per tile.  A box has to end where a page does, so its slots divide a
+// page's; a tile that no number of them fills stays partly empty.  The time of a tile grows with
+// its boxes (of K and V, a box per 64 columns in bf16) about as `fixed` + boxes, beside its share
+// of the stream: least per slot is best.  Measured for 16 x 4096 tokens in bf16, 64-, 128- and
+// 256-wide heads: pages of 20, full tiles of 4-slot boxes 52, 48 and 49 us, tiles of 60 of 64,
+// 30 of 32 and 10 of 16 slots 32, 34 and 41; pages of 24, full tiles of 8-slot boxes 38, 36 and
+// 36 us, 48 of 64, 24 of 32 and 12 of 16 slots 33, 32 and 36.  In float32 the arithmetic goes
+// by whole tiles too, and a full one is worth nearly any boxes (the case at SimtWarp: 440 us with
+// eight boxes of 4 slots, 486 with three of 10, 461 with one of 20).
+void tile_boxes(int page_size, int tile, bool bf, int D, int* box, int* n) {
+  const int fixed = bf ? 16 : 256, per = bf ? D / 32 : 2;
+  int best = 0;
+  for (int d = 1; d <= std::min(page_size, tile); ++d) {
+    if (page_size % d != 0) continue;
+    const int k = tile / d, cost = fixed + per * k;
+    if (best == 0 || (int64_t)cost * *box * *n <= (int64_t)best * d * k) {
+      best = cost;
+      *box = d;
+      *n = k;
+    }
   }
-  *n = tile / *box;
 }
 
 // Tables so short that ranges end at unit borders.
@@ -1319,7 +1325,7 @@ cudaError_t launch_c(const PagedAttnArgs& a, cudaStream_t s) {
   p.rg_log = RG == 8 ? 3 : 2;
   p.by_NG = Div::of(p.NG);
   p.by_page = Div::of(a.c.page_size);
-  tile_boxes(a.c.page_size, C::TILE, &p.box, &p.nbox);
+  tile_boxes(a.c.page_size, C::TILE, C::BF, D, &p.box, &p.nbox);
   p.tile = p.box * p.nbox;
   p.by_tile = Div::of(p.tile);
   p.align = short_table(D, C::BF, (int64_t)a.c.max_pages * a.c.page_size);
