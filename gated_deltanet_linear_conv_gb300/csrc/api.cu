@@ -685,8 +685,8 @@ int gdn_paged_attn_decode_workspace_size(const gdn_attn_dims* dims, int in_dtype
   gdn_attn_dims d = *dims;
   if (d.num_seqs > 1) d.num_seqs = 1;            // the bounds come with the call: no equal split required here
   CHECK(check_attn_dims(fn, &d, nullptr));
-  *bytes = gdn::paged_attn_workspace_bytes(dims->num_seqs, dims->total_tokens, dims->num_q_heads, dims->num_kv_heads,
-                                           dims->head_dim, in_dtype == GDN_BF16, table_tokens);
+  *bytes = gdn::paged_attn_workspace_bytes(dims->num_q_heads, dims->num_kv_heads, dims->head_dim, in_dtype == GDN_BF16,
+                                           table_tokens);
   return GDN_OK;
 }
 
@@ -702,8 +702,8 @@ int gdn_paged_attn_decode(const gdn_attn_dims* dims, const int32_t* cu_seqlens, 
   if (gate != nullptr) CHECK(check_heads(fn, "gate", gate, in_dtype));
   CHECK(check_cache(fn, dims, cache, in_dtype));
   REQUIRE_PTR(o);
-  const size_t need = gdn::paged_attn_workspace_bytes(dims->num_seqs, dims->total_tokens, dims->num_q_heads,
-                                                      dims->num_kv_heads, dims->head_dim, in_dtype == GDN_BF16,
+  const size_t need = gdn::paged_attn_workspace_bytes(dims->num_q_heads, dims->num_kv_heads, dims->head_dim,
+                                                      in_dtype == GDN_BF16,
                                                       (int64_t)cache->max_pages * cache->page_size);
   if (need > 0 && (workspace == nullptr || workspace_bytes < need || !aligned16(workspace)))
     return fail(GDN_ERR_INVALID_ARG, "%s: workspace of %zu bytes (16-byte aligned) required, got %zu", fn, need,

@@ -1241,14 +1241,17 @@ paged_attn_join_few_kernel(const __grid_constant__ Params p, int ctas) {
 // of eight (with more heads, eight rows mean fewer octets).
 int octet_rows(int Nq, int Nkv, bool bf) { return !bf && Nq / Nkv <= 4 ? 4 : 8; }
 
-// Octets per pass: enough for the new tokens of an even batch (a unit's rows then read
-// the cache once), up to as many as the registers hold the outputs of.  In float32 a
-// pass of four takes 1.7 times one of two (16 x 4096 tokens, 128-wide heads: 87 and 50 us), so
-// twos where the last four would be half empty (153 sequences with 6 octets: 46 against 55 us).
+// Octets per pass at most: as many as the registers hold the outputs (float32: and queries) of.
+int most_octets(int rg, int D, bool bf) { return bf ? 4 : std::min(rg == 8 ? 2 : 4, 2048 / (D * rg)); }
+
+// Octets per pass: enough for the new tokens of an even batch (a unit's rows then read the cache
+// once).  In float32 a pass of four takes 1.7 times one of two (16 x 4096 tokens, 128-wide heads:
+// 87 and 50 us), so twos where the last four would be half empty (153 sequences with 6 octets: 46
+// against 55 us).
 int octets_per_pass(int num_seqs, int total, int Nq, int Nkv, int D, bool bf) {
   const int rg = octet_rows(Nq, Nkv, bf);
   const int64_t want = (int64_t)((total + num_seqs - 1) / num_seqs) * ((Nq / Nkv + rg - 1) / rg);
-  const int most = bf ? 4 : std::min(rg == 8 ? 2 : 4, 2048 / (D * rg));
+  const int most = most_octets(rg, D, bf);
   int nt = 1;
   while (nt < want && nt < most) nt *= 2;
   if (!bf && nt == 4 && want > 4 && (want - 1) % 4 < 2) nt = 2;
@@ -1377,9 +1380,11 @@ cudaError_t launch_f32(const PagedAttnArgs& a, int nt, cudaStream_t s) {
 
 }  // namespace
 
-size_t paged_attn_workspace_bytes(int num_seqs, int total, int Nq, int Nkv, int D, bool bf, int64_t table_tokens) {
+// For the most rows of a pass, so that one workspace serves calls of any numbers of tokens.
+size_t paged_attn_workspace_bytes(int Nq, int Nkv, int D, bool bf, int64_t table_tokens) {
   if (short_table(D, bf, table_tokens)) return 0;
-  const size_t rows = octets_per_pass(num_seqs, total, Nq, Nkv, D, bf) * 8;
+  const int rg = octet_rows(Nq, Nkv, bf);
+  const size_t rows = (size_t)most_octets(rg, D, bf) * rg;
   const size_t grid = std::min(kOcc * num_sms(), kMaxCtas);
   return align16(sizeof(SplitRec) * grid) + align16(2 * grid * rows * 2 * 4) + 2 * grid * rows * D * 4;
 }

@@ -45,7 +45,7 @@ struct PagedAttnArgs {
   void* ws;
   int* err;
 };
-size_t paged_attn_workspace_bytes(int num_seqs, int total, int Nq, int Nkv, int D, bool bf, int64_t table_tokens);
+size_t paged_attn_workspace_bytes(int Nq, int Nkv, int D, bool bf, int64_t table_tokens);
 cudaError_t launch_paged_attn(const PagedAttnArgs& p, cudaStream_t s);
 
 // Launch that may begin while the kernel before it on the stream still runs: the kernel has to

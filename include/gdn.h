@@ -506,8 +506,9 @@ int gdn_paged_kv_append(const gdn_attn_dims* dims, const int32_t* cu_seqlens,
  *              (may be NULL when that is 0), no initialisation needed; not to
  *              be shared by calls that can run at the same time.  The size is
  *              for the current device and for tables of up to table_tokens =
- *              max_pages * page_size cache entries: it is 0 for short tables,
- *              and the same for all others.
+ *              max_pages * page_size cache entries: it is 0 for short tables
+ *              and the same for all others, and depends on the heads, D and the
+ *              type, not on the numbers of sequences and tokens.
  * ------------------------------------------------------------------------ */
 int gdn_paged_attn_decode_workspace_size(const gdn_attn_dims* dims, int in_dtype, int64_t table_tokens,
                                          size_t* bytes);

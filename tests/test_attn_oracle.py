@@ -145,6 +145,15 @@ def test_workspace_too_small_is_refused(gdn):
     assert b'workspace' in gdn.lib().gdn_last_error_string()
 
 
+@pytest.mark.parametrize('dtype', [torch.bfloat16, torch.float32])
+def test_one_workspace_serves_any_number_of_tokens(gdn, dtype):
+    """Calls pick their rows per pass by the tokens per sequence; the size has to be that of the most."""
+    for Nq, Nkv, D in ((8, 2, 64), (8, 2, 128), (8, 1, 128), (16, 2, 256), (4, 4, 256)):
+        sizes = {gdn.paged_attn_decode_workspace_size(n, n * t, Nq, Nkv, D, dtype, 1 << 20)
+                 for n in (1, 7, 256) for t in range(1, 10)}
+        assert len(sizes) == 1 and sizes.pop() > 0
+
+
 def test_no_tokens_is_no_work(gdn):
     assert _rope(gdn, T=0) == _append(gdn, T=0) == _attn(gdn, T=0) == gdn.GDN_OK
 

@@ -318,6 +318,18 @@ def test_several_new_tokens_in_tiles_that_are_not_full(P, D, G, n, dtype):
     check_attn(c, q, lens, new, out_dtype=dtype)
 
 
+@pytest.mark.parametrize('dtype', [BF, F32])
+def test_one_workspace_for_calls_of_any_number_of_tokens(dtype):
+    lens = [1200, 333, 700]
+    c = Cache(lens, 1, 16, 128, dtype).fill(lens, 37)
+    n = gdn.paged_attn_decode_workspace_size(3, 3 * 9, 4, 1, 128, dtype, c.bt.shape[1] * c.P)
+    ws = torch.full((n,), 255, dtype=torch.uint8, device='cuda')
+    for t in range(1, 10):
+        q = rand(38 + t, 3 * t, 4, 128, dtype=dtype)
+        y = run_attn(c, q, lens, [t] * 3, out_dtype=dtype, workspace=ws)
+        assert torch.equal(y, check_attn(c, q, lens, [t] * 3, out_dtype=dtype))
+
+
 @pytest.mark.parametrize('D,dtype', [(64, BF), (128, BF), (256, BF), (64, F32), (128, F32), (256, F32)])
 def test_later_tokens_never_reach_a_row(D, dtype):
     """NaN and infinities in a later new token's key and value leave the earlier rows as they are."""
