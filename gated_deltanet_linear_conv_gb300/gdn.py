@@ -565,7 +565,8 @@ def paged_kv_append(k, v, k_cache, v_cache, block_table, kv_lens, q=None, cos_si
 
 
 def paged_attn_decode_workspace_size(num_seqs, total, Nq, Nkv, D, dtype, table_tokens):
-    """Bytes for calls of these sizes and type over tables of up to ``table_tokens`` cache entries."""
+    """Bytes for calls of these heads and type over tables of up to ``table_tokens`` cache entries (the numbers
+    of sequences and tokens do not matter)."""
     n = _SZ(0)
     _check(lib().gdn_paged_attn_decode_workspace_size(gdn_attn_dims(num_seqs, total, Nq, Nkv, D),
                                                       GDN_BF16 if dtype == torch.bfloat16 else GDN_F32,
@@ -575,7 +576,7 @@ def paged_attn_decode_workspace_size(num_seqs, total, Nq, Nkv, D, dtype, table_t
 
 @functools.lru_cache(maxsize=256)
 def _attn_workspace_size(device, *sizes):
-    return paged_attn_decode_workspace_size(*sizes)
+    return paged_attn_decode_workspace_size(1, 1, *sizes)
 
 
 def paged_attn_decode(q, k_cache, v_cache, block_table, kv_lens, scale=None, gate=None, cu_seqlens=None,
@@ -598,7 +599,7 @@ def paged_attn_decode(q, k_cache, v_cache, block_table, kv_lens, scale=None, gat
     o = torch.empty(shape, dtype=out_dtype, device=q.device) if o is None else _given(o, shape, dev, 'o')
     ws = 0
     if workspace is None:
-        ws_bytes = _attn_workspace_size(dev, num_seqs, T, Nq, Nkv, D, dtype, block_table.shape[1] * k_cache.shape[2])
+        ws_bytes = _attn_workspace_size(dev, Nq, Nkv, D, dtype, block_table.shape[1] * k_cache.shape[2])
         if ws_bytes > 0:
             workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=q.device)
             ws = workspace.data_ptr()
