@@ -180,9 +180,9 @@ int check_cache(const char* fn, const gdn_attn_dims* d, const gdn_paged_cache* c
     if (stride[i] < span) return fail(GDN_ERR_INVALID_ARG, "%s: the cache's strides make entries overlap", fn);
     if (i > 0 && stride[i] % stride[i - 1] != 0)
       return fail(GDN_ERR_UNSUPPORTED, "%s: the cache's strides are not multiples of one another", fn);
-    span = stride[i] * ext[order[i]];
-    if (span / ext[order[i]] != stride[i] || span > ((int64_t)1 << 60))
+    if (stride[i] > ((int64_t)1 << 60) / ext[order[i]])              // (their product may pass 64 bits)
       return fail(GDN_ERR_INVALID_ARG, "%s: the cache's strides span more than 2^60 elements", fn);
+    span = stride[i] * ext[order[i]];
   }
   return GDN_OK;
 }

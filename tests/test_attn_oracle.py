@@ -214,3 +214,12 @@ def test_binding_refusals(gdn):
         gdn._norm_rope(torch.zeros(32), None, 1e-6, None, None, False, 2, 64, -1)
     with pytest.raises(ValueError, match='share'):
         gdn.qk_norm_rope(q, q.float())
+
+
+@pytest.mark.parametrize('pages,ps', [(1 << 26, 1 << 38), (1 << 30, 1 << 34), ((1 << 30) + 1, 1 << 34), (1 << 23, (1 << 38) + (1 << 20))])
+@pytest.mark.parametrize('call', ['append', 'attn'])
+def test_strides_that_span_more_than_any_memory_are_refused(gdn, call, pages, ps):
+    """Also where the product of a stride and its extent passes 64 bits."""
+    st = {'append': _append, 'attn': _attn}[call](gdn, pages=pages, ps=ps)
+    assert st == gdn.GDN_ERR_INVALID_ARG
+    assert b'span' in gdn.lib().gdn_last_error_string(), gdn.lib().gdn_last_error_string()
