@@ -579,10 +579,9 @@ def _attn_workspace_size(device, *sizes):
     return paged_attn_decode_workspace_size(1, 1, *sizes)
 
 
-def paged_attn_decode(q, k_cache, v_cache, block_table, kv_lens, scale=None, gate=None, cu_seqlens=None,
-                      out_dtype=torch.bfloat16, o=None, workspace=None):
-    """gdn_paged_attn_decode: attention of the new tokens q [tokens, Nq, D] (one or a few per sequence, bounds
-    from cu_seqlens, else equally many) over the cache, times sigmoid(gate) when given.  Returns o."""
+def _attn_call(q, k_cache, v_cache, block_table, kv_lens, scale, gate, cu_seqlens, out_dtype, o, workspace):
+    """Checks the arguments of paged_attn_decode; the library call's, the output and the workspace (to be held
+    until the call is made)."""
     T, Nq, D = shape = q.shape
     dtype = q.dtype
     if k_cache.dtype is not dtype or (gate is not None and (gate.dtype is not dtype or gate.shape != shape)):
@@ -606,9 +605,17 @@ def paged_attn_decode(q, k_cache, v_cache, block_table, kv_lens, scale=None, gat
     else:
         ws_bytes = workspace.numel() * workspace.element_size()
         ws = _given(workspace, workspace.shape, dev, 'workspace').data_ptr()
-    st = _fn('gdn_paged_attn_decode')(
-        _pack_dims(num_seqs, T, Nq, Nkv, D), cu, _heads(q, dev, 'q'), _heads(gate, dev, 'gate'), _dt(q), cache,
-        1.0 / math.sqrt(D) if scale is None else scale, o.data_ptr(), _dt(o), ws, ws_bytes, _stream())
+    return (_pack_dims(num_seqs, T, Nq, Nkv, D), cu, _heads(q, dev, 'q'), _heads(gate, dev, 'gate'), _dt(q), cache,
+            _F(1.0 / math.sqrt(D) if scale is None else scale), o.data_ptr(), _dt(o), ws, ws_bytes, _stream()), o, workspace
+
+
+def paged_attn_decode(q, k_cache, v_cache, block_table, kv_lens, scale=None, gate=None, cu_seqlens=None,
+                      out_dtype=torch.bfloat16, o=None, workspace=None):
+    """gdn_paged_attn_decode: attention of the new tokens q [tokens, Nq, D] (one or a few per sequence, bounds
+    from cu_seqlens, else equally many) over the cache, times sigmoid(gate) when given.  Returns o."""
+    args, o, workspace = _attn_call(q, k_cache, v_cache, block_table, kv_lens, scale, gate, cu_seqlens, out_dtype, o,
+                                    workspace)
+    st = _fn('gdn_paged_attn_decode')(*args)
     if st:
         _check(st, 'gdn_paged_attn_decode')
     return o
@@ -619,13 +626,32 @@ def attention_decode(q, k, v, k_cache, v_cache, block_table, kv_lens, cos_sin=No
                      out_dtype=torch.bfloat16, bufs=None):
     """One step of a full-attention layer from its projections to the input of its output projection, the
     counterpart of decode_fused in a hybrid decoder's other layers: paged_kv_append (k and v into the cache, q
-    and k normed and rotated) -> paged_attn_decode (with the output gate).
+    and k normed and rotated) -> paged_attn_decode (with the output gate).  What either call refuses is refused
+    before the cache changes.
 
     ``bufs`` (optional dict) supplies preallocated q, o, workspace."""
-    if gate is not None and (gate.dtype is not k_cache.dtype or gate.shape != q.shape):
-        raise ValueError('gate has the dtype of the cache and the shape of q')   # before the cache changes
     bufs = bufs or {}
-    qr = paged_kv_append(k, v, k_cache, v_cache, block_table, kv_lens, q, cos_sin, q_norm_w, k_norm_w, positions,
-                         cu_seqlens, norm_eps, interleaved, k_cache.dtype, bufs.get('q'))
-    return paged_attn_decode(qr, k_cache, v_cache, block_table, kv_lens, scale, gate, cu_seqlens, out_dtype,
-                             bufs.get('o'), bufs.get('workspace'))
+    qr = bufs.get('q')
+    if qr is None:
+        qr = torch.empty(q.shape, dtype=k_cache.dtype, device=q.device)
+    elif qr.shape != q.shape or not qr.is_contiguous():
+        raise ValueError('the q buffer is contiguous and has the shape of q')
+    T, Nq, D = q.shape
+    args, o, workspace = _attn_call(qr, k_cache, v_cache, block_table, kv_lens, scale, gate, cu_seqlens, out_dtype,
+                                    bufs.get('o'), bufs.get('workspace'))
+    # what only the library itself would find wrong with the attention's own arguments
+    for t, what in ((o, 'o'), (workspace, 'workspace'), (gate, 'gate')):
+        if t is not None and t.data_ptr() % 16:
+            raise ValueError('%s must be 16-byte aligned' % what)
+    if gate is not None and any(n > 1 and s * gate.element_size() % 16 for n, s in zip((T, Nq), gate.stride())):
+        raise ValueError('the strides of gate must be multiples of 16 bytes')
+    need = _attn_workspace_size(qr.get_device(), Nq, k_cache.shape[1], D, qr.dtype,
+                                block_table.shape[1] * k_cache.shape[2])
+    if T > 0 and args[10] < need:
+        raise ValueError('a workspace of %d bytes required, got %d' % (need, args[10]))
+    paged_kv_append(k, v, k_cache, v_cache, block_table, kv_lens, q, cos_sin, q_norm_w, k_norm_w, positions, cu_seqlens,
+                    norm_eps, interleaved, q_out=qr)
+    st = _fn('gdn_paged_attn_decode')(*args)
+    if st:
+        _check(st, 'gdn_paged_attn_decode')
+    return o
