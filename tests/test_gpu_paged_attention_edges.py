@@ -70,3 +70,60 @@ def test_layer_step_with_buffers_equals_its_two_calls():
     z1 = gdn.paged_attn_decode(q[:1], d.k, d.v, d.block_table[:1], lens[:1], 0.2, gate[:1], out_dtype=F32)
     gdn.check_device_error()
     assert torch.equal(y1, z1)
+
+
+# ------------------------------------------------------------------ bad metadata: what the rest of the call holds
+
+@pytest.mark.parametrize('dtype', [BF, F32])
+@pytest.mark.parametrize('width', [3, 300])          # tables with and without a split over the length
+def test_a_bad_page_reads_as_zeros(dtype, width):
+    H, P, D, lens = 2, 16, 64, [40, 17, 48]
+    c = Cache(lens, H, P, D, dtype).fill(lens, 201)
+    q = rand(202, 3, 8, D, dtype=dtype)
+    K, V = (np.concatenate([np64(x), np.zeros((1, H, P, D))]) for x in (c.k, c.v))
+    bt = np.zeros((3, width), dtype=np.int64)
+    bt[:, :3] = c.bt
+    for s, p, bad in ((0, 0, -1), (0, 2, c.pages), (1, 1, 1 << 30), (2, 1, -2 ** 31)):
+        given, zero = bt.copy(), bt.copy()
+        given[s, p], zero[s, p] = bad, c.pages       # (the oracle's caches have a page of zeros at their end)
+        y = gdn.paged_attn_decode(q, c.k, c.v, i32(given), i32(lens), out_dtype=dtype)
+        with pytest.raises(RuntimeError, match='device error 3'):
+            gdn.check_device_error()
+        ref = A.attention(np64(q), K, V, zero, [0, 1, 2, 3], lens, 1 / math.sqrt(D))
+        close_attn(y, ref, max(lens), D, dtype, dtype, (s, p, bad))
+
+
+@pytest.mark.parametrize('dtype', [BF, F32])
+@pytest.mark.parametrize('width', [3, 300])
+def test_bad_bounds_leave_their_rows_and_the_others_are_right(dtype, width):
+    """Sequences whose bounds pass the number of tokens, or end before they start, are skipped: their rows of every
+    output stay as they were, and the consistent sequences get what they get in a good call."""
+    H, G, P, D, T = 2, 4, 16, 64, 6
+    lens = [40, 17, 48]
+    tab = rope_table(64, 32)
+    q, k, v = rand(211, T, H * G, D, dtype=dtype), rand(212, T, H, D, dtype=dtype), rand(213, T, H, D, dtype=dtype)
+    bt = np.zeros((3, width), dtype=np.int64)
+    for bad_cu, good_cu, kept in (([0, 3, 9, 6], [0, 3, 6, 6], [0, 1, 2]), ([0, 3, 2, 1], [0, 3, 6, 6], [0, 1, 2]),
+                                  ([1, 3, 5, 6], [0, 3, 5, 6], [3, 4, 5]), ([0, -1, 2, 6], [0, 0, 2, 6], [2, 3, 4, 5])):
+        rest = [t for t in range(T) if t not in kept]
+        got = []
+        for cu in (bad_cu, good_cu):
+            c = Cache(lens, H, P, D, dtype).fill(lens, 214)
+            bt[:, :3] = c.bt
+            out = [torch.full((T, H * G, D), 7.0, dtype=dtype, device='cuda') for _ in range(3)]
+            calls = [lambda: gdn.qk_norm_rope(q, cos_sin=tab, cu_seqlens=i32(cu), q_out=out[0]),
+                     lambda: gdn.paged_kv_append(k, v, c.k, c.v, i32(bt), i32(lens), q, tab, cu_seqlens=i32(cu), q_out=out[1]),
+                     lambda: gdn.paged_attn_decode(q, c.k, c.v, i32(bt), i32(lens), cu_seqlens=i32(cu), o=out[2])]
+            for i, call in enumerate(calls):
+                if i == 2:                           # attention over one and the same cache
+                    c.fill(lens, 214)
+                call()
+                if cu is bad_cu:
+                    with pytest.raises(RuntimeError, match='device error 1'):
+                        gdn.check_device_error()
+                else:
+                    gdn.check_device_error()
+            got.append(out)
+        for y, z in zip(*got):
+            assert torch.equal(y[kept], z[kept]), bad_cu
+            assert (y[rest] == 7).all(), bad_cu
