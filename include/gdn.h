@@ -475,7 +475,7 @@ int gdn_qk_norm_rope(const gdn_attn_dims* dims, const int32_t* cu_seqlens,
  *   cache          written in cache_dtype; read: block_table and kv_lens
  * Nothing is written for an inactive sequence (kv_lens = 0; q_out neither) nor
  * for a token whose metadata raised the error flag.  Two tokens that map to
- * one slot leave either one's values there.
+ * one slot leave a mix of their rows there, in pieces of 16 bytes.
  * ------------------------------------------------------------------------ */
 int gdn_paged_kv_append(const gdn_attn_dims* dims, const int32_t* cu_seqlens,
                         const gdn_heads* q, const gdn_heads* k, const gdn_heads* v,

@@ -127,3 +127,34 @@ def test_bad_bounds_leave_their_rows_and_the_others_are_right(dtype, width):
         for y, z in zip(*got):
             assert torch.equal(y[kept], z[kept]), bad_cu
             assert (y[rest] == 7).all(), bad_cu
+
+
+# ------------------------------------------------------------------ norm + rotation over its own input, slots written twice
+
+@pytest.mark.parametrize('T,Nq,Nkv,D,rot,inter', [(1, 16, 2, 256, 64, False), (77, 6, 3, 64, 64, False),
+                                                  (300, 32, 8, 128, 128, False), (41, 40, 1, 128, 96, True)])
+@pytest.mark.parametrize('dtype', [BF, F32])
+def test_norm_rope_in_place(T, Nq, Nkv, D, rot, inter, dtype):
+    q, k, tab = rand(221, T, Nq, D, dtype=dtype), rand(222, T, Nkv, D, dtype=dtype), rope_table(T, rot)
+    w = 1 + rand(223, D, dtype=F32, std=0.2)
+    qo, ko = gdn.qk_norm_rope(q, k, tab, w, w, interleaved=inter, out_dtype=dtype)
+    q1, k1, q2 = q.clone(), k.clone(), q.clone()
+    gdn.qk_norm_rope(q1, k1, tab, w, w, interleaved=inter, q_out=q1, k_out=k1)
+    assert torch.equal(q1, qo) and torch.equal(k1, ko)
+    c = Cache([T], Nkv, 16, D, dtype)
+    gdn.paged_kv_append(k, k, c.k, c.v, c.block_table, i32([T]), q2, tab, w, w, interleaved=inter, q_out=q2)
+    gdn.check_device_error()
+    assert torch.equal(q2, qo)
+
+
+def test_two_sequences_that_append_to_one_slot():
+    """What is left there is made of the two rows; nothing else is touched."""
+    c = Cache([16] * 32, 2, 16, 128, BF)
+    c.bt[:, 0] = c.bt[0, 0]
+    k, v = rand(231, 32, 2, 128), rand(232, 32, 2, 128)
+    gdn.paged_kv_append(k, v, c.k, c.v, i32(c.bt), i32([5] * 32))
+    gdn.check_device_error()
+    for x, y in ((c.k, k), (c.v, v)):
+        row = x[int(c.bt[0, 0]), :, 4].reshape(2, 16, 1, 8)           # 16-byte pieces
+        assert (row == y.reshape(32, 2, 16, 8).permute(1, 2, 0, 3)).all(-1).any(-1).all()
+        assert int((~x.isnan()).sum()) == 2 * 128
