@@ -158,3 +158,98 @@ def test_two_sequences_that_append_to_one_slot():
         row = x[int(c.bt[0, 0]), :, 4].reshape(2, 16, 1, 8)           # 16-byte pieces
         assert (row == y.reshape(32, 2, 16, 8).permute(1, 2, 0, 3)).all(-1).any(-1).all()
         assert int((~x.isnan()).sum()) == 2 * 128
+
+
+# ------------------------------------------------------------------ caches in other orders
+
+@pytest.mark.parametrize('order', [(1, 0, 2, 3), (2, 0, 1, 3), (2, 1, 0, 3), (1, 2, 0, 3)])
+@pytest.mark.parametrize('dtype', [BF, F32])
+@pytest.mark.parametrize('P', [16, 20])
+def test_any_order_of_pages_heads_and_slots(order, dtype, P):
+    """Memory in the given order of the axes page 0, head 1, slot 2."""
+    H, D, lens = 3, 128, [150, 33, 0, 7]
+    c = Cache(lens, H, P, D, dtype)
+    shape = (c.pages, H, P, D)
+    back = [order.index(i) for i in range(4)]
+    c.k, c.v = (torch.full([shape[i] for i in order], float('nan'), dtype=dtype, device='cuda').permute(back)
+                for _ in range(2))
+    assert c.k.shape == shape
+    k, v, T = rand(241, 190, H, D, dtype=dtype), rand(242, 190, H, D, dtype=dtype), 190
+    cu = i32([0, 150, 183, 183, 190])
+    gdn.paged_kv_append(k, v, c.k, c.v, c.block_table, i32(lens), cu_seqlens=cu)
+    gdn.check_device_error()
+    assert int((~c.k.isnan()).sum()) == k.numel() and int((~c.v.isnan()).sum()) == v.numel()
+    q = rand(243, T, 2 * H, D, dtype=dtype)
+    check_attn(c, q, lens, [150, 33, 0, 7], out_dtype=dtype)
+
+
+# ------------------------------------------------------------------ one workspace, many calls
+
+@pytest.mark.parametrize('dtype', [BF, F32])
+@pytest.mark.parametrize('N,most', [(1, 9000), (20, 2000), (100, 900)])          # few cut units, some, many
+def test_calls_in_flight_on_one_workspace(dtype, N, most):
+    """Calls of other lengths, inputs and numbers of tokens one behind the other, without a wait between them: each
+    gives what it gives alone with a workspace of its own."""
+    H, G, D, P = 2, 4, 128, 16
+    rng = np.random.default_rng(N)
+    calls, width = [], (most + P - 1) // P
+    for i, t in enumerate((1, 1, 2, 1, 4)):
+        lens = [int(x) for x in rng.integers(most // 2, most, N)]
+        c = Cache(lens, H, P, D, dtype, seed=i)
+        c.k.copy_(rand(250 + i, *c.k.shape, dtype=dtype))
+        c.v.copy_(rand(260 + i, *c.v.shape, dtype=dtype))
+        bt = np.zeros((N, width), dtype=np.int64)
+        bt[:, :c.bt.shape[1]] = c.bt
+        calls.append((rand(270 + i, N * t, H * G, D, dtype=dtype), c.k, c.v, i32(bt), i32(lens)))
+    alone = []
+    for a in calls:
+        alone.append(gdn.paged_attn_decode(*a, out_dtype=dtype))
+        torch.cuda.synchronize()
+    n = gdn.paged_attn_decode_workspace_size(N, N, H * G, H, D, dtype, width * P)
+    ws = torch.full((n,), 255, dtype=torch.uint8, device='cuda')
+    order = rng.integers(0, len(calls), 120).tolist()
+    outs = [gdn.paged_attn_decode(*calls[i], out_dtype=dtype, workspace=ws) for i in order]
+    gdn.check_device_error()
+    for i, y in zip(order, outs):
+        assert torch.equal(y, alone[i]), i
+
+
+def test_a_gate_made_on_another_stream_beside_the_append():
+    """Fork before the append, join before the attention; eager, and captured into a graph."""
+    N, H, D = 8, 2, 128
+    lens = [int(x) for x in np.random.default_rng(3).integers(1, 1000, N)]
+    c = Cache([1000] * N, H, 16, D, BF).fill(lens, 281)
+    q, k, v, src = rand(282, N, 8, D), rand(283, N, H, D), rand(284, N, H, D), rand(285, N, 8, D)
+    gate, big, n = src.clone(), rand(286, 2048, 2048, dtype=F32), i32(lens)
+    side, own = torch.cuda.Stream(), torch.cuda.Stream()
+
+    def step():
+        main = torch.cuda.current_stream()
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            x = big @ big                            # some time before the gate is there
+            gate.copy_(src + 0 * x[:1, :1].to(BF))
+        gdn.paged_kv_append(k, v, c.k, c.v, c.block_table, n)
+        main.wait_stream(side)
+        return gdn.paged_attn_decode(q, c.k, c.v, c.block_table, n, gate=gate)
+
+    gdn.paged_kv_append(k, v, c.k, c.v, c.block_table, n)
+    ref = gdn.paged_attn_decode(q, c.k, c.v, c.block_table, n, gate=gate)
+    torch.cuda.synchronize()
+    for _ in range(10):
+        gate.zero_()
+        assert torch.equal(step(), ref)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(own):
+        step()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=own):
+        y = step()
+    for _ in range(10):
+        gate.zero_()
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, ref)
+    gdn.check_device_error()
