@@ -223,3 +223,26 @@ def test_strides_that_span_more_than_any_memory_are_refused(gdn, call, pages, ps
     st = {'append': _append, 'attn': _attn}[call](gdn, pages=pages, ps=ps)
     assert st == gdn.GDN_ERR_INVALID_ARG
     assert b'span' in gdn.lib().gdn_last_error_string(), gdn.lib().gdn_last_error_string()
+
+
+@pytest.mark.parametrize('n,D,dtype', [(131072, 256, torch.bfloat16), (65537, 64, torch.bfloat16), (40009, 128, torch.float32)])
+def test_a_lost_or_doubled_tile_of_a_long_context_is_seen(n, D, dtype):
+    """The GPU test of long contexts rejects an answer that lacks a tile, or a CTA's piece, or has it twice."""
+    from test_gpu_paged_attention_edges import close_shares, position_values
+
+    rng = np.random.default_rng(2)
+    k, q, v = rng.standard_normal((n, D)), rng.standard_normal(D), position_values(n, D)
+    x = k @ q / math.sqrt(D)
+    w = np.exp(x - x.max())
+    smax = (np.abs(k) @ np.abs(q)).max(keepdims=True) / math.sqrt(D)
+    y = (w / w.sum()) @ v
+    near = lambda z: close_shares(torch.tensor(z)[None].to(dtype), (y[None], y[None], smax), n, 2, D, dtype, dtype, 304)  # noqa: E731
+    near(y)
+    tile = 8192 // (D * dtype.itemsize)
+    for length in (tile, 862 // tile * tile):
+        for t0 in (0, 10 * tile, n // 2 // tile * tile, n - length):
+            for times in (0.0, 2.0):
+                z = w.copy()
+                z[t0:t0 + length] *= times
+                with pytest.raises(AssertionError):
+                    near((z / z.sum()) @ v)

@@ -253,3 +253,34 @@ def test_a_gate_made_on_another_stream_beside_the_append():
         torch.cuda.synchronize()
         assert torch.equal(y, ref)
     gdn.check_device_error()
+
+
+# ------------------------------------------------------------------ long contexts, each tile's share
+
+def position_values(n, D):
+    """Values [n, D] of which a row names its place: token j has a one in column j D / n.  A column of the output
+    then is the weight of its stretch of tokens, and a tile that is lost or counted twice changes it."""
+    v = np.zeros((n, D))
+    v[np.arange(n), np.arange(n) * D // n] = 1.0
+    return v
+
+
+def close_shares(y, ref, n, units, D, in_dtype, out_dtype, ctas, what=''):
+    """With values >= 0 the mass is the output itself, so the bound is relative.  The longest chain of additions into one sum
+    is a CTA's share of the tokens (rounded up to tiles of up to 64), then the pieces of a unit, at most one per CTA."""
+    close_attn(y, ref, -(-n * units // ctas) + 64 + ctas, D, in_dtype, out_dtype, what)
+
+
+@pytest.mark.parametrize('D,H,dtype,n,P', [(256, 2, BF, 131072, 64), (128, 1, BF, 100003, 20), (64, 3, BF, 65537, 16),
+                                           (128, 1, F32, 40009, 24), (256, 1, F32, 30000, 64)])
+def test_every_tile_of_a_long_context_counts_once(D, H, dtype, n, P):
+    c = Cache([n], H, P, D, dtype)
+    c.k.copy_(rand(291, *c.k.shape, dtype=dtype))
+    v = np.zeros((c.bt.shape[1] * P, D))
+    v[:n] = position_values(n, D)
+    c.v[c.block_table[0].long()] = torch.tensor(v, dtype=dtype, device='cuda').reshape(-1, 1, P, D)
+    q = rand(292, 1, 4 * H, D, dtype=dtype)
+    y = run_attn(c, q, [n], [1], out_dtype=dtype, cu=False)
+    ref = A.attention(np64(q), np64(c.k), np64(c.v), c.bt, [0, 1], [n], 1 / math.sqrt(D))
+    ctas = 2 * torch.cuda.get_device_properties(0).multi_processor_count
+    close_shares(y, ref, n, H, D, dtype, dtype, ctas)
