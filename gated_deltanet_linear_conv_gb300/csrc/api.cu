@@ -243,6 +243,38 @@ int norm_rope(const char* fn, const gdn_attn_dims* dims, const int32_t* cu, cons
   return GDN_OK;
 }
 
+// gdn_paged_attn_decode, and the test hook of its waits (wait_ns > 0).
+int attn_decode(const char* fn, const gdn_attn_dims* dims, const int32_t* cu_seqlens, const gdn_heads* q,
+                const gdn_heads* gate, int in_dtype, const gdn_paged_cache* cache, float scale, void* o, int out_dtype,
+                void* workspace, size_t workspace_bytes, int64_t wait_ns, int skip, void* stream) {
+  CHECK(check_attn_dims(fn, dims, cu_seqlens));
+  if (!valid_dtype(in_dtype) || !valid_dtype(out_dtype)) return fail(GDN_ERR_INVALID_ARG, "%s: bad dtype", fn);
+  if (dims->total_tokens == 0) return GDN_OK;
+  CHECK(check_heads(fn, "q", q, in_dtype));
+  if (gate != nullptr) CHECK(check_heads(fn, "gate", gate, in_dtype));
+  CHECK(check_cache(fn, dims, cache, in_dtype));
+  REQUIRE_PTR(o);
+  const size_t need = gdn::paged_attn_workspace_bytes(dims->num_q_heads, dims->num_kv_heads, dims->head_dim,
+                                                      in_dtype == GDN_BF16,
+                                                      (int64_t)cache->max_pages * cache->page_size);
+  if (need > 0 && (workspace == nullptr || workspace_bytes < need || !aligned16(workspace)))
+    return fail(GDN_ERR_INVALID_ARG, "%s: workspace of %zu bytes (16-byte aligned) required, got %zu", fn, need,
+                workspace_bytes);
+  int* flag = nullptr;
+  CHECK(get_flag(&flag));
+  gdn::PagedAttnArgs p{};
+  p.q = heads_in(q); p.gate = heads_in(gate); p.c = paged_cache(dims, cache); p.o = o;
+  p.cu = cu_seqlens; p.num_seqs = dims->num_seqs; p.total = dims->total_tokens;
+  p.Nq = dims->num_q_heads; p.Nkv = dims->num_kv_heads; p.D = dims->head_dim;
+  p.scale = scale; p.in_bf16 = in_dtype == GDN_BF16; p.out_bf16 = out_dtype == GDN_BF16;
+  p.ws = workspace; p.err = flag;
+  if (wait_ns > 0) p.wait_ns = (unsigned long long)wait_ns;
+  p.skip = skip;
+  cudaError_t e = gdn::launch_paged_attn(p, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, fn);
+  return GDN_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -694,31 +726,19 @@ int gdn_paged_attn_decode(const gdn_attn_dims* dims, const int32_t* cu_seqlens, 
                           const gdn_heads* gate, int in_dtype, const gdn_paged_cache* cache,
                           float scale, void* o, int out_dtype, void* workspace,
                           size_t workspace_bytes, void* stream) {
-  const char* fn = "gdn_paged_attn_decode";
-  CHECK(check_attn_dims(fn, dims, cu_seqlens));
-  if (!valid_dtype(in_dtype) || !valid_dtype(out_dtype)) return fail(GDN_ERR_INVALID_ARG, "%s: bad dtype", fn);
-  if (dims->total_tokens == 0) return GDN_OK;
-  CHECK(check_heads(fn, "q", q, in_dtype));
-  if (gate != nullptr) CHECK(check_heads(fn, "gate", gate, in_dtype));
-  CHECK(check_cache(fn, dims, cache, in_dtype));
-  REQUIRE_PTR(o);
-  const size_t need = gdn::paged_attn_workspace_bytes(dims->num_q_heads, dims->num_kv_heads, dims->head_dim,
-                                                      in_dtype == GDN_BF16,
-                                                      (int64_t)cache->max_pages * cache->page_size);
-  if (need > 0 && (workspace == nullptr || workspace_bytes < need || !aligned16(workspace)))
-    return fail(GDN_ERR_INVALID_ARG, "%s: workspace of %zu bytes (16-byte aligned) required, got %zu", fn, need,
-                workspace_bytes);
-  int* flag = nullptr;
-  CHECK(get_flag(&flag));
-  gdn::PagedAttnArgs p{};
-  p.q = heads_in(q); p.gate = heads_in(gate); p.c = paged_cache(dims, cache); p.o = o;
-  p.cu = cu_seqlens; p.num_seqs = dims->num_seqs; p.total = dims->total_tokens;
-  p.Nq = dims->num_q_heads; p.Nkv = dims->num_kv_heads; p.D = dims->head_dim;
-  p.scale = scale; p.in_bf16 = in_dtype == GDN_BF16; p.out_bf16 = out_dtype == GDN_BF16;
-  p.ws = workspace; p.err = flag;
-  cudaError_t e = gdn::launch_paged_attn(p, static_cast<cudaStream_t>(stream));
-  if (e != cudaSuccess) return cuda_fail(e, fn);
-  return GDN_OK;
+  return attn_decode("gdn_paged_attn_decode", dims, cu_seqlens, q, gate, in_dtype, cache, scale, o, out_dtype, workspace,
+                     workspace_bytes, 0, 0, stream);
+}
+
+int gdn_test_paged_attn_wait_timeout(const gdn_attn_dims* dims, const int32_t* cu_seqlens, const gdn_heads* q,
+                                     int in_dtype, const gdn_paged_cache* cache, void* o, void* workspace,
+                                     size_t workspace_bytes, int64_t wait_ns, int skip, void* stream) {
+  const char* fn = "gdn_test_paged_attn_wait_timeout";
+  if (wait_ns < 1000000 || wait_ns > 10000000000ll)
+    return fail(GDN_ERR_INVALID_ARG, "%s: wait_ns must lie in [1 ms, 10 s]", fn);
+  if (skip < 1 || skip > 3) return fail(GDN_ERR_INVALID_ARG, "%s: skip must be 1, 2 or 3", fn);
+  return attn_decode(fn, dims, cu_seqlens, q, nullptr, in_dtype, cache, 1.0f, o, in_dtype, workspace, workspace_bytes,
+                     wait_ns, skip, stream);
 }
 
 }  // extern "C"

@@ -45,7 +45,6 @@ constexpr int kMinTiles = 4;                       // tiles of a range at least 
 constexpr int kUnitCost = 4;                       // a unit's start and join, in tiles, where ranges are cut
 constexpr int kOcc = 2;                            // CTAs per SM
 constexpr int kMaxCtas = 512;                      // CTAs, and so pieces of a unit, at most
-constexpr uint64_t kWaitNs = 2000000000ull;        // bound of every wait
 constexpr uint32_t kPollCap = 1u << 28;
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -144,18 +143,18 @@ __device__ __forceinline__ uint64_t now_ns() {
 
 // Bounded wait of a whole warp on a phase; gives up when another warp aborted or the time
 // ran out, all lanes alike.
-__device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, volatile int* abort) {
+__device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, volatile int* abort, uint64_t limit) {
   const uint64_t t0 = now_ns();
 #pragma unroll 1
   for (uint32_t i = 0; i < kPollCap; ++i) {
     if (tc::mbar_try_wait(bar, parity)) return true;
-    if (*abort != 0 || now_ns() - t0 > kWaitNs) break;
+    if (*abort != 0 || now_ns() - t0 > limit) break;
   }
   return false;
 }
-__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, volatile int* abort) {
+__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, volatile int* abort, uint64_t limit) {
   bool ok = tc::mbar_try_wait(bar, parity);
-  if (!ok) ok = wait_slow(bar, parity, abort);
+  if (!ok) ok = wait_slow(bar, parity, abort, limit);
   return __all_sync(0xffffffffu, ok);
 }
 
@@ -765,6 +764,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
     // ------------------------------------------------------------ producer
     SplitRec rec{};
     int it = 0, npiece = 0;
+    const int boxes = a.skip & 2 ? 0 : p.nbox;     // (no copies: the test of waits that run out)
     bool ok = true;
     if (lo < hi) {
       int s = from_seq[0];
@@ -813,13 +813,13 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
         for (int tile = t0; tile < t1; ++tile, ++it) {
           int npage = 0, noff = 0;
           const int st = it % C::STAGES;
-          ok = wait_bar(empty + st, ((it / C::STAGES) & 1) ^ 1, abort);
+          ok = wait_bar(empty + st, ((it / C::STAGES) & 1) ^ 1, abort, p.a.wait_ns);
           if (!ok) break;
           uint8_t* kd = ring + st * 2 * kStageHalf;
           if (lane == 0) tc::mbar_arrive_expect_tx(full + st, p.tile * (2 * kStageHalf / C::TILE));
           __syncwarp();
 #pragma unroll 1
-          for (int b = lane; b < p.nbox; b += 32) {
+          for (int b = lane; b < boxes; b += 32) {
             if (b >= 32) lookup(tile, b, page, off);
             auto axis = [&](int i) { return a.c.order[i] == 0 ? off : a.c.order[i] == 1 ? kvh : page; };
 #pragma unroll
@@ -835,7 +835,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
           if (tile != t0) continue;
           // behind its first tile: the piece and its query rows.  Octet x of the sequence is token
           // x / NG, heads (x % NG) * 8 .. of the kv head's G
-          ok = wait_bar(qempty, (npiece & 1) ^ 1, abort);
+          ok = wait_bar(qempty, (npiece & 1) ^ 1, abort, p.a.wait_ns);
           if (!ok) {
             ++it;                                  // (this tile is in flight)
             break;
@@ -864,7 +864,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
 #pragma unroll 1
           for (int r = lane; r < nvalid * RG; r += 32) {
             const int h = head_of(r, tok);
-            if (h < p.G) {
+            if (h < p.G && !(a.skip & 1)) {
               tc::bulk_load(qs + r * C::QPITCH,
                             static_cast<const T*>(a.q.p) + (q.bos + tok) * a.q.ts + (kvh * p.G + h) * a.q.hs,
                             D * sizeof(T), qfull);
@@ -884,7 +884,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
       }
     }
     if (ok) {
-      ok = wait_bar(qempty, (npiece & 1) ^ 1, abort);
+      ok = wait_bar(qempty, (npiece & 1) ^ 1, abort, p.a.wait_ns);
       if (ok && lane == 0) {
         piece->tile0 = -1;
         tc::mbar_arrive(qfull);
@@ -898,8 +898,8 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
     // every copy lands before the CTA's shared memory goes, whatever the consumers do
     int none = 0;
 #pragma unroll 1
-    for (int i = max(0, it - C::STAGES); i < it; ++i) wait_bar(full + i % C::STAGES, (i / C::STAGES) & 1, &none);
-    if (!ok && npiece > 0) wait_bar(qfull, (npiece - 1) & 1, &none);
+    for (int i = max(0, it - C::STAGES); i < it; ++i) wait_bar(full + i % C::STAGES, (i / C::STAGES) & 1, &none, p.a.wait_ns);
+    if (!ok && npiece > 0) wait_bar(qfull, (npiece - 1) & 1, &none, p.a.wait_ns);
     return;
   }
 
@@ -918,11 +918,13 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
   const int turn = C::BF || C::SL < C::TG ? C::SL : (p.tile + C::SLICE - 1) / C::SLICE;
   typename WarpOf<T, D, NT, RG>::type w;
   int it = 0;
-  // After a wait that ran out a warp carries on with what the stages hold until the next
-  // barrier of all consumers, where they agree to stop: no barrier is left short of a warp.
+  // After a wait that ran out a warp leaves its piece and goes to the next barrier of all consumers,
+  // where they agree to stop; on the way it meets the warps that share its slices at each slice's
+  // barrier, so that none is left short of a warp.  It hands no stage back: one that did not fill
+  // must not be armed again.
 #pragma unroll 1
   for (int np = 0;; ++np) {
-    bool ok = wait_bar(qfull, np & 1, abort);
+    bool ok = wait_bar(qfull, np & 1, abort, p.a.wait_ns);
     if (tc::named_sync_or(1, C::CW * 32, !ok)) {
       if (lane == 0) {
         *abort = 1;
@@ -943,9 +945,17 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
       int j = (tw - it * turn) & (C::TG - 1);      // this warp's first slice of the stage
       if (j >= C::SL) continue;
       const int st = it % C::STAGES;
-      if (!wait_bar(full + st, (it / C::STAGES) & 1, abort)) {
+      if (!wait_bar(full + st, (it / C::STAGES) & 1, abort, p.a.wait_ns)) {
         ok = false;
-        if (lane == 0) *abort = 1;                 // ends the waits that follow at once
+        if (lane == 0) *abort = 1;                 // ends the waits of the others
+        if (C::DS > 1) {
+#pragma unroll 1
+          for (; tile < d.tile1; ++tile, ++it)
+#pragma unroll 1
+            for (j = (tw - it * turn) & (C::TG - 1); j < C::SL; j += C::TG)
+              if (tile * p.tile + j * C::SLICE < min(most, (tile + 1) * p.tile)) tc::named_sync(2 + tw, C::DS * 32);
+        }
+        break;
       }
       uint8_t* kd = ring + st * 2 * kStageHalf;
 #pragma unroll 1

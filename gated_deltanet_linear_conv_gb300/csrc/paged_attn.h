@@ -44,6 +44,8 @@ struct PagedAttnArgs {
   int in_bf16, out_bf16;
   void* ws;
   int* err;
+  unsigned long long wait_ns = 2000000000ull;    // bound of every wait
+  int skip = 0;                                  // test hook: copies never issued (1 query rows, 2 keys and values)
 };
 size_t paged_attn_workspace_bytes(int Nq, int Nkv, int D, bool bf, int64_t table_tokens);
 cudaError_t launch_paged_attn(const PagedAttnArgs& p, cudaStream_t s);

@@ -28,7 +28,7 @@ EXPORTS = ('gdn_version', 'gdn_last_error_string', 'gdn_check_device_error', 'gd
            'gdn_recurrent_decode', 'gdn_recurrent_decode_steps',
            'gdn_gated_rmsnorm', 'gdn_decode_fused',
            'gdn_qk_norm_rope', 'gdn_paged_kv_append', 'gdn_paged_attn_decode_workspace_size',
-           'gdn_paged_attn_decode', 'gdn_test_chunk_wait_timeout')
+           'gdn_paged_attn_decode', 'gdn_test_chunk_wait_timeout', 'gdn_test_paged_attn_wait_timeout')
 
 
 class gdn_dims(ctypes.Structure):
@@ -96,6 +96,7 @@ _SIGS = {
     'gdn_paged_kv_append': ([_ADIMS, _P, _HEADS, _HEADS, _HEADS, _I, _NR, _CACHE, _I, _P, _I, _P], _I),
     'gdn_paged_attn_decode_workspace_size': ([_ADIMS, _I, _I64, ctypes.POINTER(_SZ)], _I),
     'gdn_paged_attn_decode': ([_ADIMS, _P, _HEADS, _HEADS, _I, _CACHE, _F, _P, _I, _P, _SZ, _P], _I),
+    'gdn_test_paged_attn_wait_timeout': ([_ADIMS, _P, _HEADS, _I, _CACHE, _P, _P, _SZ, _I64, _I, _P], _I),
     'gdn_test_chunk_wait_timeout': ([_DIMS, _P, _P, _P, _P, _P, _P, _P, _SZ, _I64, _P], _I),
 }
 

@@ -541,6 +541,17 @@ int gdn_test_chunk_wait_timeout(const gdn_dims* dims, const void* q, const void*
                                 const float* g, const float* beta, void* o, void* workspace,
                                 size_t workspace_bytes, int64_t wait_ns, void* stream);
 
+/* gdn_test_paged_attn_wait_timeout enqueues gdn_paged_attn_decode (o in
+ * in_dtype, no gate, scale 1) with copies that are never issued although the
+ * kernel waits for them (skip: 1 query rows, 2 keys and values, 3 both), and
+ * with each wait bounded by wait_ns (1 ms .. 10 s): every CTA with work gives
+ * up, lets what it has in flight land, raises the device error flag with code 2
+ * and exits.  What o then holds is undefined. */
+int gdn_test_paged_attn_wait_timeout(const gdn_attn_dims* dims, const int32_t* cu_seqlens,
+                                     const gdn_heads* q, int in_dtype, const gdn_paged_cache* cache,
+                                     void* o, void* workspace, size_t workspace_bytes,
+                                     int64_t wait_ns, int skip, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
