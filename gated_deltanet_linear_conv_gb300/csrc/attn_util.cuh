@@ -22,8 +22,8 @@ __device__ __forceinline__ void check_seqs(const int32_t* cu, int num_seqs, int 
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void pdl_launch_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
-// x / d for 0 <= x < 2^31 by one multiplication (d > 0): with 2^k the first power of two that is
-// at least d and m = floor(2^32 (2^k - d) / d) + 1, x / d = (hi32(x m) + x) >> k.
+// x / d for 0 <= x < 2^31 by one multiplication (d > 0; Granlund and Montgomery's division by an
+// invariant integer): with 2^k the first power of two that is at least d and m = floor(2^32 (2^k - d) / d) + 1, x / d = (hi32(x m) + x) >> k.
 struct Div {
   uint32_t d, m, k;
   static Div of(uint32_t d) {

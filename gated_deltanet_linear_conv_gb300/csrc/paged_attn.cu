@@ -2,15 +2,19 @@
 // full-attention layers and section "Cache"):
 //   o[t, h] = sum_j softmax_j(scale q[t, h] . k_j) v_j, then * sigmoid(gate[t, h]).
 //
-// Bound: every visible key and value is read once per call and used by the G = Nq / Nkv
-// query heads of its head, 2 G flops per byte in bf16 and G in float32 for each new token:
+// Bound: a pass reads every key and value of a sequence and kv head once, for the G = Nq / Nkv
+// query heads of that head, 2 G flops per byte in bf16 and G in float32 for each new token:
 // in bf16 far below the matrix ridge, so the kernel is a stream of the cache at HBM rate with
-// the softmax riding along (one pass, running maximum and sum).  float32 is that for one
-// token; with more, the CUDA cores bound it.
+// the softmax riding along (running maximum and sum).  float32 is that for one token; with
+// more, the CUDA cores bound it.
 //
 // Rows.  The 8 columns of a product tile (an octet) are query heads of one token and one
-// kv head; all its columns see the same cache indices.  A unit is (sequence, kv head, NT
-// consecutive octets); its cache indices split into tiles of 8 KB of K and 8 KB of V.
+// kv head; all its columns see the same cache indices.  A unit is one pass: (sequence, kv head,
+// NT consecutive octets); its cache indices split into tiles of at most 8 KB of K and 8 KB of V.
+// A sequence with more octets per kv head (more than four in bf16, fewer in float32) takes more
+// passes, and each streams the whole sequence: also tiles behind the last index that the pass's
+// tokens see, which the consumers skip.  With a few new tokens that is next to nothing; for a
+// whole prompt it is half of the traffic.
 //
 // Work split.  All tiles of all units, laid end to end with a gap of kUnitCost for each
 // unit's start and join, are cut into one equal range per CTA (two CTAs per SM, one's starts
@@ -19,17 +23,28 @@
 // captured graph needs the lengths.  A unit inside one
 // range is finished by its CTA; the pieces of a unit that crosses ranges (at most one cut
 // per CTA) go to the workspace, unnormalised with their maxima and sums, and a second small
-// kernel joins them in order.  With short tables (no unit can exceed kAlignTiles tiles)
-// ranges end at unit borders instead and no second kernel runs.
+// kernel joins them in order.  With short tables (at most kAlignTiles full tiles of tokens; fewer
+// than twice as many tiles where pages do not fill a tile) ranges end at unit borders instead
+// and no second kernel runs.
+//
+// Where the time goes, from copies of the kernel that leave a step out (us; 16 sequences of 512 to
+// 8192 with four tokens, 16 heads over 2 of 256 | one sequence of 131072, the same heads | float32,
+// 32 sequences of 100 to 4000, 8 heads over 2 of 128): stream with its start and end 23.7 | 44.2 |
+// 26.0 (at the copy rate 17.3 | 40.3 | 20.5), arithmetic 4.1 | 2.4 | 2.1 more, pieces to the workspace 2.1
+// | 0.6 | 0, their join 6.5 | 4.4 | 2.8; together 36.5 | 51.7 | 30.7.
 //
 // Inside a CTA a producer warp walks the range: it looks the page ids up and issues TMA
-// boxes that end where pages do (slots past the end of a sequence come as the out-of-range
+// boxes that end where pages do (boxes past the end of a sequence come as the out-of-range
 // zero fill) into a ring of stages, and the query rows of each unit by bulk copies.  Four
 // consumer warps take 16-token (bf16) or 4-token (float32) slices with a maximum, sum and
 // output of their own, joined through shared memory once per unit.  With many rows in bf16
 // (NT * D > 256) DS of them share a slice: each computes the weights of NT / DS octets, they
 // exchange them, and each accumulates D / DS columns of the output of all octets, so that a
 // warp never holds more than 64 accumulators.
+//
+// Why not the tensor memory's products: with keys on the 128-row side the 8 to 32 rows of a pass
+// would be their columns, and possible; but the matrix instructions used here are 12 to 33 % busy, so
+// for these calls their rate is not what bounds.  Many rows (prompts) are another matter.
 
 #include "attn_util.cuh"
 #include "paged_attn.h"
@@ -40,9 +55,19 @@ namespace gdn {
 namespace {
 
 constexpr int kStageHalf = 8192;                   // bytes of K (and of V) in a stage
-constexpr int kAlignTiles = 16;                    // no unit longer than this: ranges end at unit borders
-constexpr int kMinTiles = 4;                       // tiles of a range at least (fewer CTAs for little work)
-constexpr int kUnitCost = 4;                       // a unit's start and join, in tiles, where ranges are cut
+// Tables of at most so many full tiles: ranges end at unit borders, no workspace.  Whole units against
+// cut ones in bf16, us: 64 sequences of 8 tiles 12.6 and 14.5 (256-wide heads), 11.8 and 12.2
+// (128-wide); of 16 tiles 19.2 and 17.5, 18.0 and 15.5; one sequence of 16 tiles 16.7 and 11.1; 64
+// of 32 tiles 31 and 23.  The cut is the faster one from somewhat below 16 tiles on; the limit is
+// also what tables need no workspace by, and stays.
+constexpr int kAlignTiles = 16;
+// Tiles of a range at least: fewer CTAs for little work, so fewer pieces to join.  1, 2, 4, 8 and 16: one
+// sequence of 600 tokens, 2 kv heads of 256, 10.0, 10.1, 11.3, 14.3 and 19.8 us; 8 of 2000 of 128 11.5,
+// 11.5, 11.5, 14.1 and 19.6.
+constexpr int kMinTiles = 4;
+// A unit's start and join, in tiles, where ranges are cut.  0, 2, 4 and 8: 700 sequences of 1 to 1500
+// tokens 110, 101.7, 103.6 and 110 us; 16 x 4 tokens of 512 to 8192 38.4, 36.8, 36.5 and 36.6.
+constexpr int kUnitCost = 4;
 constexpr int kOcc = 2;                            // CTAs per SM
 constexpr int kMaxCtas = 512;                      // CTAs, and so pieces of a unit, at most
 constexpr uint32_t kPollCap = 1u << 28;
@@ -1051,7 +1076,10 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
 // ------------------------------------------------------------------ the join
 // Launched while the main kernel runs; the first step is to wait for its end.  Three forms,
 // by how many units can be cut at most, so that neither blocks start for nothing nor many
-// pieces wait for one another.
+// pieces wait for one another.  The whole call with the third form below, with PG = 4 and with PG =
+// 1, us, bf16, 131072 tokens in all, so many units of 256-wide heads: 1 unit 33, 45 and 65; 2 52, 58 and 69; 8
+// 51, 52 and 55; 16 53.5, 51.3 and 52.0; 32 57.7, 50.9 and 51.3; 128 81, 53.5 and 51.1; with more units
+// than half of the CTAs, 160 (PG = 4: 54.8) and 256 (57.9), PG = 1 takes 51.2 and 52.2.
 //
 // PG = 1, about as many units as CTAs (about two pieces each): blocks (c, y) join the unit that starts
 // in CTA c's range and ends behind it, if there is one; a thread takes four columns of a row.
@@ -1185,7 +1213,7 @@ paged_attn_join_few_kernel(const __grid_constant__ Params p, int ctas) {
   const int row = blockIdx.y, oct = row >> p.rg_log, x = r.x0 + oct, t = p.by_NG.quot(x);
   const int h = ((x - t * p.NG - oct) << p.rg_log) + row;
   if (oct >= r.nvalid || h >= p.G) return;
-  constexpr int U = 5;                             // (two units over 304 CTAs: all of their 152 pieces at once)
+  constexpr int U = 5;                             // loads in flight per thread (2, 3 and 10: all calls within 1 us)
   const int k = tid / LPR, col = (tid % LPR) * 4, e = blockIdx.z * 64 + col, n = r.pieces;
   float v[U][4];
 #pragma unroll
@@ -1291,7 +1319,8 @@ void tile_boxes(int page_size, int tile, bool bf, int D, int* box, int* n) {
   }
 }
 
-// Tables so short that ranges end at unit borders.
+// Tables so short that ranges end at unit borders, by full tiles: the page size is not known where
+// the workspace's size is asked for.
 bool short_table(int D, bool bf, int64_t table_tokens) {
   return table_tokens <= (int64_t)kAlignTiles * (kStageHalf / (D * (bf ? 2 : 4)));
 }

@@ -437,8 +437,8 @@ typedef struct {
  *                new ones: new token i of n has cache index kv_lens[s] - n + i.
  *                0 marks an inactive slot of a padded batch.
  * A length below 0, below the sequence's new tokens (unless 0) or above
- * max_pages * page_size, and a page id outside [0, num_pages), raise the
- * device error flag. */
+ * max_pages * page_size (the attention's limit is also 2^31 - 256), and a page
+ * id outside [0, num_pages), raise the device error flag. */
 typedef struct {
   void* k;
   void* v;
@@ -492,12 +492,17 @@ int gdn_paged_kv_append(const gdn_attn_dims* dims, const int32_t* cu_seqlens,
  * Rows of an inactive sequence (kv_lens = 0) and of one whose kv_lens raised
  * the error flag are zero; a page id that raised it reads as zeros.  Cache
  * entries past a token's own index never reach its row, whatever they hold.
- * Scores, softmax statistics and sums are float32.
+ * Scores, softmax statistics and sums are float32.  With a bf16 cache the
+ * weights enter the product with v as the sum of two bf16 values, 16 bits of
+ * them (2^-16 relative to sum_j p_j |v_j|: below the rounding of a bf16 o, to be
+ * seen in a float32 one).  A visible NaN, or an infinite v, makes what it
+ * enters NaN or infinite (with a bf16 cache NaN also where an infinite v alone
+ * would give infinity).
  *
- * Made for one or a few new tokens per sequence (decode, draft + verify):
- * every 8 (token, query head) rows of a key/value head are one tile of the
- * products, a few tiles share one pass over the cache, and a sequence with
- * more new tokens takes more passes.
+ * Made for one or a few new tokens per sequence (decode, draft + verify): up
+ * to 8 query heads of one token and one key/value head are one tile of the
+ * products (float32: up to 4 or 8), a few tiles share one pass over the
+ * sequence's whole cache, and a sequence with more tokens takes more passes.
  *
  *   q, gate    [tokens, Nq, D]   in_dtype (strided); gate may be NULL
  *   cache      in_dtype
@@ -508,7 +513,8 @@ int gdn_paged_kv_append(const gdn_attn_dims* dims, const int32_t* cu_seqlens,
  *              for the current device and for tables of up to table_tokens =
  *              max_pages * page_size cache entries: it is 0 for short tables
  *              and the same for all others, and depends on the heads, D and the
- *              type, not on the numbers of sequences and tokens.
+ *              type, not on the numbers of sequences and tokens (20 MB at most
+ *              on 152 SMs; one token may use as little as a quarter of it).
  * ------------------------------------------------------------------------ */
 int gdn_paged_attn_decode_workspace_size(const gdn_attn_dims* dims, int in_dtype, int64_t table_tokens,
                                          size_t* bytes);
