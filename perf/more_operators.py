@@ -238,7 +238,7 @@ def _quantised(gen, pages, nkv, P, d):
     """A cache of normal keys or values, by pages so that little float32 is held at a time."""
     c = torch.empty(pages, nkv, P, d // 2, dtype=torch.uint8, device='cuda')
     s = torch.empty(pages, nkv, P, d // GROUP, 2, dtype=torch.bfloat16, device='cuda')
-    step = max(1, (1 << 27) // (nkv * P * d))
+    step = max(1, (1 << 28) // (nkv * P * d))
     for a in range(0, pages, step):
         x = torch.randn(min(step, pages - a), nkv, P, d, generator=gen, device='cuda')
         c[a:a + step], s[a:a + step] = _quantise(x)
@@ -370,14 +370,13 @@ def _verify_plain(st):
 
 
 def _quantise(x):
-    """[..., d] -> bytes [..., d/2], scales [..., d/64, 2].  Values lie next to where a rounding turns: in 64 bits."""
-    x = x.double()
+    """float32 [..., d] -> bytes [..., d/2], scales [..., d/64, 2]."""
     g = x.unflatten(-1, (-1, GROUP))
     lo, hi = g.amin(-1, keepdim=True), g.amax(-1, keepdim=True)
     # quotients of short numbers meet borders: true divisions (by a tensor), halves to even
-    s = ((hi - lo) / torch.full_like(lo, 15.0)).float().bfloat16()
-    m = lo.float().bfloat16()
-    n = ((g - m.double()) / torch.where(s > 0, s.double(), math.inf)).round_().clamp_(0.0, 15.0).to(torch.uint8).flatten(-2)
+    s = ((hi - lo) / torch.full_like(lo, 15.0)).bfloat16()
+    m = lo.bfloat16()
+    n = ((g - m.float()) / torch.where(s > 0, s.float(), math.inf)).round_().clamp_(0.0, 15.0).to(torch.uint8).flatten(-2)
     return n[..., 0::2] | (n[..., 1::2] << 4), torch.cat([s, m], -1)
 
 
@@ -388,9 +387,9 @@ def _values(c, s):
     return (n * s[..., :1] + s[..., 1:]).flatten(-2)
 
 
-def _norm_rope_plain(x, w, cs, inter, dtype=torch.float32):
-    """x [T, H, D] -> dtype; w [D] or None; cs [T, r] or None (the table rows of the tokens)."""
-    u = x.to(dtype)
+def _norm_rope_plain(x, w, cs, inter):
+    """x [T, H, D] -> float32; w [D] or None; cs [T, r] or None (the table rows of the tokens)."""
+    u = x.float()
     if w is not None:
         u = u * torch.rsqrt((u * u).mean(-1, keepdim=True) + 1e-6) * w
     if cs is None:
@@ -431,8 +430,8 @@ def _append_plain(st):
     case = st['case']
     page, slot, pos, some = _places(st)
     cs = st['table'][pos.clamp_min(0)] if st['table'] is not None else None
-    k = _norm_rope_plain(st['k'], st['k_w'], cs, case['inter'], torch.float64)
-    for x, c, s in ((k, 'kc', 'ks'), (st['v'], 'vc', 'vs')):
+    k = _norm_rope_plain(st['k'], st['k_w'], cs, case['inter'])
+    for x, c, s in ((k, 'kc', 'ks'), (st['v'].float(), 'vc', 'vs')):
         st[c][page, :, slot], st[s][page, :, slot] = _quantise(x)
     return (_norm_rope_plain(st['q'], st['q_w'], cs, case['inter']).to(st['dt']),) + _read_plain(st)
 
@@ -609,8 +608,8 @@ def _held_exact(x):
     for a in range(0, x.shape[-1], GROUP):
         g = x[..., a:a + GROUP]
         least = g.min(-1, keepdim=True).values
-        step = ((g.max(-1, keepdim=True).values - least) / 15.0).float().bfloat16().double()
-        base = least.float().bfloat16().double()
+        step = ((g.max(-1, keepdim=True).values - least) / 15.0).bfloat16().double()
+        base = least.bfloat16().double()
         n = torch.round((g - base) / torch.where(step > 0, step, 1.0)).clamp(0, 15)
         out[..., a:a + GROUP] = base + n * step
     return out
