@@ -84,7 +84,7 @@ struct Cfg {
   static constexpr int RING = kWarps * STAGES * STAGE;
   static constexpr int JP = D + 4;                 // join row pitch (floats)
   static constexpr int JOIN = kWarps * 8 * (JP + 2) * 4;
-  static constexpr int Q = NT * NG * 1024;         // q operands
+  static constexpr int Q = NT * NG * 1024 + ROWS * 4;              // q operands, and a factor of each row's products
   static constexpr int SMEM = (RING > JOIN ? RING : JOIN) + Q;
   static_assert((SMEM + 1024) * OCC <= 228 * 1024 && STAGE % 128 == 0 && KV % 128 == 0, "ring");   // (addresses within a stage go by xor)
 };
@@ -255,10 +255,13 @@ struct Warp {
   uint32_t q_at;                                   // this lane's q operands: 16 bytes for each octet, group and half of it
   float vs[NT][NG][2];                             // kWeight / r, of columns 2t, 2t + 1
 
-  // Every warp of the CTA writes the same q operands to `qs_`: each reads what it wrote itself.
-  __device__ __forceinline__ void start(const Params& p, const Seq& q, int x0, int rows, int kvh, uint32_t qs_, int lane) {
+  // Every warp of the CTA writes the same q operands to `qs_`: each reads what it wrote itself.  Returns whether some row has
+  // a factor of its products, 2^part below, that is not 1: only slice<true> heeds them.
+  __device__ __forceinline__ bool start(const Params& p, const Seq& q, int x0, int rows, int kvh, uint32_t qs_, int lane) {
     q_at = qs_ + lane * 16;
     const int g = lane >> 2, t = lane & 3;
+    const uint32_t fs = qs_ + NT * NG * 1024;
+    bool far = false;
     // matrices of a group's product: tokens 0..7 and 8..15 of its first 32 elements, then of its others
     x_at = piece_at<NG>(lane & 15, lane >> 4);
     s_at = 2 * C::KV + g * (NG * 4);
@@ -292,10 +295,17 @@ struct Warp {
       }
       top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
       top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-      // by a power of two, so that the row's largest lies in [2^10, 2^11): bf16's digits all fit f16
-      const uint32_t ex = __float_as_uint(top) >> 23;
-      const uint32_t by = ex == 0 || ex == 255 ? 127 : min(254u, 264u - ex);
-      const float up = __uint_as_float(by << 23);
+      // by a power of two, so that the row's largest lies in [2^10, 2^11) (below that where float32 has no greater power):
+      // bf16's digits all fit f16
+      const int ex = (int)(__float_as_uint(top) >> 23), by = ex == 255 ? 127 : min(254, 264 - ex);
+      const float up = __uint_as_float((uint32_t)by << 23);
+      // A score is c 2^e times the sum of its products with the row, e = 24 + 127 - by.  Where queries from 2^113 on bring that
+      // factor to float32's end, the products get a part of it: a sum that leaves float32 then is one whose score does.
+      const int e2 = 151 - by, part = min(127, max(0, (int)(__float_as_uint(p.c) >> 23 & 255) + e2 - 253));
+      auto power = [](int i) { return __uint_as_float((uint32_t)(127 + i) << 23); };
+      const int e3 = e2 - part;                    // (in two steps: 2^e3 alone may leave the range)
+      const float factor = p.c * power(e3 >> 1) * power(e3 - (e3 >> 1));
+      far = far || part > 0;
 #pragma unroll
       for (int gr = 0; gr < NG; ++gr) {
         float v[16];                               // (read again: kept, the row would cost 16 NG registers)
@@ -307,7 +317,7 @@ struct Warp {
           sum[gr] += v[i];
         }
         sum[gr] += __shfl_xor_sync(0xffffffffu, sum[gr], 1);
-        sum[gr] += __shfl_xor_sync(0xffffffffu, sum[gr], 2);
+        sum[gr] = (sum[gr] + __shfl_xor_sync(0xffffffffu, sum[gr], 2)) * (5.9604644775390625e-8f * power(part));
         // of step st of half w: elements 2 st, 2 st + 4 (low nibbles), 2 st + 1, 2 st + 5 (high ones)
 #pragma unroll
         for (int w = 0; w < 2; ++w)
@@ -316,14 +326,14 @@ struct Warp {
                        "r"(pack_half(v[8 * w + 2], v[8 * w + 6])), "r"(pack_half(v[8 * w + 3] * 0.0625f, v[8 * w + 7] * 0.0625f))
                        : "memory");
       }
+      if (t == 0) asm volatile("st.shared.f32 [%0], %1;" ::"r"(fs + r * 4), "f"(power(part)) : "memory");
       // of the columns: from the lanes that hold those rows
-      const float factor = p.c * 16777216.f * __uint_as_float((254 - by) << 23);
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int from = (2 * t + e) * 4;
         cm[nt][e] = __shfl_sync(0xffffffffu, factor, from);
 #pragma unroll
-        for (int gr = 0; gr < NG; ++gr) qs[nt][gr][e] = __shfl_sync(0xffffffffu, sum[gr], from) * 5.9604644775390625e-8f;
+        for (int gr = 0; gr < NG; ++gr) qs[nt][gr][e] = __shfl_sync(0xffffffffu, sum[gr], from);
         const int c = nt * 8 + 2 * t + e;
         lim[nt][e] = c < rows ? q.len - q.n + p.by_G.quot(x0 + c) + 1 : 0;
         m[nt][e] = kLowest;
@@ -339,17 +349,24 @@ struct Warp {
           for (int e = 0; e < 4; ++e) o[nt][gr][i][e] = 0.f;
       }
     }
+    return __any_sync(0xffffffffu, far);
   }
 
-  // The tokens from tok0 in stage `at`.  TAIL: some column does not see all of them.
+  // The tokens from tok0 in stage `at`.  TAIL: some column does not see all of them, or start() said so.
   template <bool TAIL>
   __device__ __forceinline__ void slice(uint32_t at, int tok0, int lane) {
     constexpr int U = C::U;
     const int ra = lane >> 2;                      // this lane's tokens: ra and ra + 8 of each 16
     constexpr uint32_t kRow = D / 2;
     const uint32_t xat = at + x_at, sat = at + s_at;               // (a group further on is 32 bytes away by xor)
-    float s[U][NT][4];
+    float s[U][NT][4], more[NT][2];
     uint32_t ka[U][NG], kb[U][NG];
+    if (TAIL) {
+      const uint32_t f_at = q_at + NT * NG * 1024 - lane * 16 + (lane & 3) * 8;    // of columns 2t, 2t + 1 (see start)
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+        asm volatile("ld.shared.v2.f32 {%0,%1}, [%2];" : "=f"(more[nt][0]), "=f"(more[nt][1]) : "r"(f_at + nt * 32) : "memory");
+    }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       lds_words<NG>(sat + u * 16 * NG * 4, ka[u]);
@@ -384,6 +401,10 @@ struct Warp {
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
+            if (TAIL) {
+              acc[nt][e] *= more[nt][e];
+              acc[nt][2 + e] *= more[nt][e];
+            }
             const float fa = gr == 0 ? ma * qs[nt][gr][e] : fmaf(ma, qs[nt][gr][e], s[u][nt][e]);
             const float fb = gr == 0 ? mb * qs[nt][gr][e] : fmaf(mb, qs[nt][gr][e], s[u][nt][2 + e]);
             s[u][nt][e] = fmaf(sa, acc[nt][e], fa);
@@ -744,9 +765,9 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, NT>::OCC)) kv4_attn_kernel(c
         lookup(t0 + warp + (i + 1) * kWarps);
       }
       Warp<C> w;
-      w.start(p, q, x0, rows, kvh, qat, lane);
+      const bool far = w.start(p, q, x0, rows, kvh, qat, lane);
       __syncwarp();
-      const int all = q.len - q.n + p.by_G.quot(x0) + 1;           // the first row's token sees least
+      const int all = far ? 0 : q.len - q.n + p.by_G.quot(x0) + 1; // the first row's token sees least
       const int most = q.len - q.n + p.by_G.quot(x0 + rows - 1) + 1;
       int st = 0;
 #pragma unroll 1

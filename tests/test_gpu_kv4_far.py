@@ -1,0 +1,69 @@
+"""The 4-bit paged cache where its numbers are far from ordinary, and what stands beside one another in a batch."""
+
+import numpy as np
+import pytest
+import torch
+
+import oracle.serving_oracle as S
+from gated_deltanet_linear_conv_gb300 import gdn
+from helpers import np64
+from test_gpu_kv4 import BF, close4, cuts, filled, i32, kv4_reference, rand, tables
+
+pytestmark = pytest.mark.gpu
+
+
+def scaled_keys(cache, seed, std):
+    """Normal keys of that size in place of the cache's."""
+    pages, H, P, half = cache[0].shape
+    n, s, m = S.quantise(np64(rand(seed, pages, H, P, 2 * half, dtype=torch.float32)) * std)
+    cache[0].copy_(torch.from_numpy(n[..., 0::2] | n[..., 1::2] << 4))
+    cache[2].copy_(torch.from_numpy(np.stack([s, m], -1)))
+
+
+@pytest.mark.parametrize('D', [64, 128, 256])
+@pytest.mark.parametrize('qp,kp', [(113, -114), (117, -118), (121, -122), (126, -127), (-113, 110), (-117, 114), (-121, 118),
+                                   (-126, 122), (-131, 124)])
+@pytest.mark.parametrize('scale', [None, 1.0])
+def test_queries_of_any_size(D, qp, kp, scale):
+    """Queries next to either end of float32's range over keys that keep the scores ordinary, large ones beside ordinary
+    ones.  (Keys below 2^-100 have no steps: their groups are of one value each.  Queries of 2^-131 have three bits.)"""
+    P, H, G, new, lens = 16, 2, 5, [1, 3], [700, 65]
+    bt, pages = tables(3, lens, P)
+    cache = filled(11, pages, H, P, D)
+    scaled_keys(cache, 13, 2.0 ** kp * (1.0 if scale is None else D ** -0.5))
+    q = rand(17, sum(new), H * G, D, dtype=torch.float32)
+    (q[:, ::3] if qp > 0 else q).mul_(2.0 ** qp)
+    q = q.to(BF)
+    assert q.isfinite().all()
+    y = gdn.paged_kv4_attn_decode(q, *cache, i32(bt.tolist()), i32(lens), cu_seqlens=i32(cuts(new)), scale=scale)
+    close4(y, kv4_reference(q, cache, bt, cuts(new), lens, D ** -0.5 if scale is None else scale, None))
+    gdn.check_device_error()
+
+
+@pytest.mark.parametrize('D', [64, 128, 256])
+@pytest.mark.parametrize('qp', [100, 117, 121, 124])
+@pytest.mark.parametrize('scale', [None, 1.0])
+def test_scores_of_large_queries_pick_one_key(D, qp, scale):
+    """Keys with steps under such queries: the scores are finite in float32 and lie so far apart that one key takes all."""
+    P, H, G, n = 16, 1, 8, 300
+    bt, pages = tables(4, [n], P)
+    cache = filled(21, pages, H, P, D)
+    scaled_keys(cache, 23, 2.0 ** -12)
+    q = (rand(27, 1, H * G, D, dtype=torch.float32).sign() * 2.0 ** qp).to(BF)
+    y = np64(gdn.paged_kv4_attn_decode(q, *cache, i32(bt.tolist()), i32([n]), scale=scale))
+    gdn.check_device_error()
+    j = np.arange(n)
+    value = [S.values(np.stack([b & 15, b >> 4], -1).reshape(b.shape[:-1] + (D,)), s[..., 0], s[..., 1])
+             for b, s in ((c.cpu().numpy(), np64(t)) for c, t in (cache[::2], cache[1::2]))]
+    K, V = (x[bt[0][j // P], 0, j % P] for x in value)
+    x = np64(q)[0] @ K.T                                     # [heads, tokens]
+    assert np.abs(x).max() * (D ** -0.5 if scale is None else scale) * 1.5 < 2.0 ** 128
+    top = np.sort(x, -1)
+    # float32 sums of D products of size 2^qp (n s + |m|), some 5 or 6 |K|, each rounded by 2^-23 at most: further apart than
+    # their errors
+    clear = top[:, -1] - top[:, -2] > 2 * (D + 8) * 2.0 ** -23 * 2.0 ** qp * 8 * np.abs(K).sum(-1).max()
+    assert clear.sum() >= G // 2
+    want = V[x.argmax(-1)]
+    # a weight of 1 times a step in f16 (n s of it: V and the group's least value at most), and the output's half step
+    near = 2.0 ** -11 * (np.abs(V).max() * 2) + 2.0 ** -8 * np.abs(want)
+    assert (np.abs(y[0] - want) <= near)[clear].all()
