@@ -32,12 +32,17 @@ namespace {
 constexpr int kCtas = 8;
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
-constexpr uint32_t kMost = 0x7fffffffu;
+constexpr int64_t kMost = 0x7fffffff;
+constexpr uint32_t kStop = 0x80000000u;
 constexpr int kRest = GDN_PLAN_REST;
 
-__device__ __forceinline__ uint32_t sat_add(uint32_t a, uint32_t b) { return min(a + b, kMost); }    // a, b <= kMost
+__device__ __forceinline__ uint32_t sat_add(uint32_t a, uint32_t b) {          // a, b <= kStop
+  const uint32_t s = a + b;
+  return s < a ? kStop : min(s, kStop);            // (both kStop: 0)
+}
 
-// Three running sums that stop at kMost (no request that reaches it fits).
+// Three running sums that stop at kStop: above every number of tokens or pages that a call can have, so that no request
+// which reaches it fits.
 struct Sums {
   uint32_t add, take, back;
 };
@@ -82,7 +87,7 @@ __global__ void __launch_bounds__(kThreads) page_plan_kernel(const __grid_consta
         bad = bad || len != 0;
       } else if (add < 0) {
         x.back = held;
-      } else if (len < 0 || len > (int64_t)held * p.page_size || (int64_t)len + add > min(most, (int64_t)kMost)) {
+      } else if (len < 0 || len > (int64_t)held * p.page_size || (int64_t)len + add > min(most, kMost)) {
         bad = true;
       } else if (add > 0) {
         x.add = add;

@@ -1,0 +1,39 @@
+"""Step metadata where its numbers or its inputs are far from ordinary."""
+
+import pytest
+import torch
+
+from gated_deltanet_linear_conv_gb300 import gdn
+
+pytestmark = pytest.mark.gpu
+
+
+def i32(v):
+    return torch.tensor(v, dtype=torch.int32, device='cuda')
+
+
+@pytest.mark.parametrize('new,fits', [([2 ** 30 + 10] * 2, False), ([2 ** 30] * 3, False), ([2 ** 31 - 1, 1], False),
+                                      ([2 ** 30 - 1, 2 ** 30], True), ([1, 2 ** 31 - 3, 1], True), ([2 ** 31 - 2, 1], True)])
+@pytest.mark.parametrize('where', [0, 600])
+def test_plan_sums_next_to_32_bits(new, fits, where):
+    """Requests of more tokens than total_tokens = 2^31 - 1 are refused whole, those of as many are not.  (The last sequence alone
+    asking for 2^31 - 1 is PLAN_REST.)"""
+    N, P, W = where + len(new), 1 << 26, 32
+    new = [0] * where + new
+    held = [0] * N
+    lens, hold, ring, free, table = i32(held), i32(held), i32([0, 128]), torch.arange(128, dtype=torch.int32, device='cuda'), i32([[9] * W] * N)
+    out = gdn.PagedPlan(torch.empty(N + 1, dtype=torch.int32, device='cuda'), None, None, *(torch.full((n,), -7, dtype=torch.int32, device='cuda')
+                                                                                           for n in (N, N, 2)))
+    total = 2 ** 31 - 1
+    gdn.paged_plan(i32(new), lens, hold, ring, free, table, P, total, out=out)
+    if fits:
+        gdn.check_device_error()
+        pages = [-(-n // P) for n in new]
+        assert out.cu_seqlens.tolist() == [sum(new[:i]) for i in range(N + 1)] and out.kv_lens.tolist() == new
+        assert out.pages_held.tolist() == pages and out.free_ring.tolist() == [sum(pages), 128 - sum(pages)]
+        assert [p for s, n in enumerate(pages) for p in table[s, :n].tolist()] == list(range(sum(pages)))
+    else:
+        with pytest.raises(RuntimeError, match='device error 4'):
+            gdn.check_device_error()
+        assert out.cu_seqlens.tolist() == [0] * (N + 1) and out.kv_lens.tolist() == held and out.pages_held.tolist() == held
+        assert out.free_ring.tolist() == [0, 128] and (table == 9).all()
