@@ -1,4 +1,4 @@
-"""Step metadata where its numbers or its inputs are far from ordinary."""
+"""Step metadata and verification where their numbers or inputs are far from ordinary."""
 
 import pytest
 import torch
@@ -37,3 +37,19 @@ def test_plan_sums_next_to_32_bits(new, fits, where):
             gdn.check_device_error()
         assert out.cu_seqlens.tolist() == [0] * (N + 1) and out.kv_lens.tolist() == held and out.pages_held.tolist() == held
         assert out.free_ring.tolist() == [0, 128] and (table == 9).all()
+
+
+def test_verify_draft_probs_of_no_drafts():
+    """A step without drafts: the same as with none given; with drafts the call is refused."""
+    N, V = 5, 300
+    g = torch.Generator().manual_seed(1)
+    p, u = torch.softmax(torch.randn(2 * N, V, generator=g), -1).cuda(), torch.rand(2 * N, generator=g).cuda()
+    tok, none = i32([3] * (2 * N)), torch.empty(N, 0, V, device='cuda')
+    acc, out, _ = gdn.draft_verify(p[:N], tok[:N], u[:N], none, num_seqs=N)
+    assert acc.tolist() == [0] * N and torch.equal(out, gdn.draft_verify(p[:N], tok[:N], u[:N], num_seqs=N)[1])
+    gdn.draft_verify(p[:1], tok[:1], u[:1], none, cu_seqlens=i32([0, 0, 1, 1, 1, 1]))
+    gdn.draft_verify(p[:0], tok[:0], u[:0], none, cu_seqlens=i32([0] * (N + 1)))
+    for T, cu in ((2 * N, None), (N, i32([0, 2, 3, 4, 5, 5])), (N, i32([0, 1, 2, 3, 4, 5]))):
+        with pytest.raises(ValueError, match='no drafts'):
+            gdn.draft_verify(p[:T], tok[:T], u[:T], none, cu_seqlens=cu, num_seqs=N)
+    gdn.check_device_error()
