@@ -407,16 +407,17 @@ __device__ __noinline__ void quantise_closely(const float (&x)[16], int open, bo
     const bool up = k >= 8;
     todo &= todo - 1;
     const float sj = up ? s[1] : s[0];
-    const uint32_t n = ((up ? nib[1] : nib[0]) >> at) & 15u;
     const Pair d = exact(k) + Pair{-(up ? m[1] : m[0]), 0.f};
+    // from the pair: float32's own number is off by more than one where a group's range is a few of its values' last digits
+    const uint32_t n = (uint32_t)fminf(fmaxf(rintf(__fmul_rn(d.h, rcp_approx(sj))), 0.f), 15.f);
     // above (n + 1/2) s, below (n - 1/2) s, or on one of them: these differences are exact next to 0
     const float over = __fadd_rn(__fmaf_rn(-((float)n + 0.5f), sj, d.h), d.l);
     const float under = __fadd_rn(__fmaf_rn(-((float)n - 0.5f), sj, d.h), d.l);
     uint32_t to = n;                               // (off by one at most)
     if (n < 15 && (over > 0.f || (over == 0.f && n % 2 == 1))) to = n + 1;
     if (n > 0 && (under < 0.f || (under == 0.f && n % 2 == 1))) to = n - 1;
-    if (up) nib[1] ^= (n ^ to) << at;
-    else nib[0] ^= (n ^ to) << at;
+    if (up) nib[1] = (nib[1] & ~(15u << at)) | to << at;
+    else nib[0] = (nib[0] & ~(15u << at)) | to << at;
   }
   __syncwarp();
 }

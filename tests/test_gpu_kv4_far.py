@@ -4,10 +4,11 @@ import numpy as np
 import pytest
 import torch
 
+import oracle.attn_oracle as A
 import oracle.serving_oracle as S
 from gated_deltanet_linear_conv_gb300 import gdn
 from helpers import np64
-from test_gpu_kv4 import BF, close4, cuts, filled, i32, kv4_reference, rand, tables
+from test_gpu_kv4 import BF, F32, close4, cuts, filled, i32, kv4_reference, new_cache, packed, rand, rope_table, tables
 
 pytestmark = pytest.mark.gpu
 
@@ -15,8 +16,8 @@ pytestmark = pytest.mark.gpu
 def scaled_keys(cache, seed, std):
     """Normal keys of that size in place of the cache's."""
     pages, H, P, half = cache[0].shape
-    n, s, m = S.quantise(np64(rand(seed, pages, H, P, 2 * half, dtype=torch.float32)) * std)
-    cache[0].copy_(torch.from_numpy(n[..., 0::2] | n[..., 1::2] << 4))
+    n, s, m = S.quantise(np64(rand(seed, pages, H, P, 2 * half, dtype=F32)) * std)
+    cache[0].copy_(torch.from_numpy(packed(n)))
     cache[2].copy_(torch.from_numpy(np.stack([s, m], -1)))
 
 
@@ -31,7 +32,7 @@ def test_queries_of_any_size(D, qp, kp, scale):
     bt, pages = tables(3, lens, P)
     cache = filled(11, pages, H, P, D)
     scaled_keys(cache, 13, 2.0 ** kp * (1.0 if scale is None else D ** -0.5))
-    q = rand(17, sum(new), H * G, D, dtype=torch.float32)
+    q = rand(17, sum(new), H * G, D, dtype=F32)
     (q[:, ::3] if qp > 0 else q).mul_(2.0 ** qp)
     q = q.to(BF)
     assert q.isfinite().all()
@@ -49,7 +50,7 @@ def test_scores_of_large_queries_pick_one_key(D, qp, scale):
     bt, pages = tables(4, [n], P)
     cache = filled(21, pages, H, P, D)
     scaled_keys(cache, 23, 2.0 ** -12)
-    q = (rand(27, 1, H * G, D, dtype=torch.float32).sign() * 2.0 ** qp).to(BF)
+    q = (rand(27, 1, H * G, D, dtype=F32).sign() * 2.0 ** qp).to(BF)
     y = np64(gdn.paged_kv4_attn_decode(q, *cache, i32(bt.tolist()), i32([n]), scale=scale))
     gdn.check_device_error()
     j = np.arange(n)
@@ -67,3 +68,26 @@ def test_scores_of_large_queries_pick_one_key(D, qp, scale):
     # a weight of 1 times a step in f16 (n s of it: V and the group's least value at most), and the output's half step
     near = 2.0 ** -11 * (np.abs(V).max() * 2) + 2.0 ** -8 * np.abs(want)
     assert (np.abs(y[0] - want) <= near)[clear].all()
+
+
+@pytest.mark.parametrize('D', [64, 128, 256])
+@pytest.mark.parametrize('weight', [1.0, 1.5, -2.0])
+@pytest.mark.parametrize('spread', [1e-7, 2e-7, 1e-6, 3e-5])
+def test_append_bits_of_nearly_constant_rows(D, weight, spread):
+    """float32 rows whose groups span a few of their values' last digits, through a norm of equal weights: the stored bits are
+    float64's, although float32 is off by whole steps."""
+    T, P = 96, 16
+    g = torch.Generator().manual_seed(D)
+    base = torch.tensor([5.0, -3.0, 1000.0, 0.01, 1.0, 7e4])[torch.arange(T) % 6][:, None, None]
+    k = (base * (1 + spread * torch.randn(T, 1, D, generator=g))).cuda()
+    w = torch.full((D,), weight, device='cuda')
+    bt, pages = tables(3, [T], P)
+    at = np.arange(T)
+    for rot in (0, 32):                                      # (what is rotated spreads; the groups behind it do not)
+        cache, tab = new_cache(pages, 1, P, D), rope_table(T, rot) if rot else None
+        gdn.paged_kv4_append(k, k, *cache, i32(bt.tolist()), i32([T]), cos_sin=tab, k_norm_w=w)
+        gdn.check_device_error()
+        n, s, m = S.quantise(A.norm_rope(np64(k), np64(w), float(np.float32(1e-6)), np64(tab), list(range(T)), False))
+        assert np.array_equal(np64(cache[2])[bt[0][at // P], :, at % P], np.stack([s, m], -1).astype(np.float64))
+        got = cache[0].cpu().numpy()[bt[0][at // P], :, at % P]
+        assert np.array_equal(got, packed(n)), (rot, np.argwhere(got != packed(n))[:4].tolist())
