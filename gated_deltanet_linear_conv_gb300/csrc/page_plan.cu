@@ -186,7 +186,9 @@ __global__ void __launch_bounds__(kThreads) page_plan_kernel(const __grid_consta
 #pragma unroll 1
   for (int i = me; i < n_back; i += all) {
     const int s = owner(given, N, i);
-    p.free_pages[free_at(count + i)] = p.bt[(int64_t)s * p.max_pages + (i - given[s])];
+    const int pg = p.bt[(int64_t)s * p.max_pages + (i - given[s])];
+    if (pg < 0 || pg >= p.num_pages) raise_error(p.err, kDevErrCache);
+    p.free_pages[free_at(count + i)] = pg;
   }
   // the state's update, once every CTA has read what it needs
   cluster.sync();

@@ -648,8 +648,9 @@ int gdn_paged_kv4_attn_decode(const gdn_attn_dims* dims, const int32_t* cu_seqle
  * or the state is inconsistent (kv_lens above pages_held * page_size, below 0, more
  * pages free and given back than there are, ...),
  * the device error flag is raised, the state stays as it was and the step has no
- * tokens.  A page id outside [0, num_pages) raises the flag; the slots of its
- * tokens are -1.
+ * tokens.  A page id outside [0, num_pages) that a new token needs, or that is taken or
+ * given back, raises the flag; the slots of its tokens are -1, and it stays where it
+ * is, in the table or in the ring.
  * At most 16384 sequences (else GDN_ERR_UNSUPPORTED).
  * ------------------------------------------------------------------------ */
 #define GDN_PLAN_REST 0x7fffffff

@@ -53,3 +53,25 @@ def test_verify_draft_probs_of_no_drafts():
         with pytest.raises(ValueError, match='no drafts'):
             gdn.draft_verify(p[:T], tok[:T], u[:T], none, cu_seqlens=cu, num_seqs=N)
     gdn.check_device_error()
+
+
+@pytest.mark.parametrize('bad', [-1, 12, 2 ** 31 - 1])
+@pytest.mark.parametrize('seqs', [3, 700])
+def test_plan_page_out_of_range_given_back(bad, seqs):
+    """An ended sequence's page that is none of the cache's is flagged when it goes back, not when it is given out."""
+    new, held = [-1] + [0] * (seqs - 1), [2] + [0] * (seqs - 1)
+    table = torch.zeros(seqs, 3, dtype=torch.int32, device='cuda')
+    table[0, :2] = i32([3, bad])
+    for row, flagged in ((0, True), (seqs - 1, False)):      # of a sequence that has ended, or lies idle
+        free = torch.full((12,), -9, dtype=torch.int32, device='cuda')
+        t, n, h = table.clone(), list(new), list(held)
+        if row:
+            t[row], t[0], n[row], h[row] = table[0], i32([3, 4, 0]), 0, 2
+        out = gdn.paged_plan(i32(n), i32([5 if x else 0 for x in h]), i32(h), i32([11, 0]), free, t, 4, 0)
+        if flagged:
+            with pytest.raises(RuntimeError, match='device error 3'):
+                gdn.check_device_error()
+        else:
+            gdn.check_device_error()
+        assert out.free_ring.tolist() == [11, 2] and [int(free[11]), int(free[0])] == [3, bad if flagged else 4]
+        assert out.pages_held.tolist()[0] == 0 and out.kv_lens.tolist()[0] == 0
