@@ -91,3 +91,57 @@ def test_append_bits_of_nearly_constant_rows(D, weight, spread):
         assert np.array_equal(np64(cache[2])[bt[0][at // P], :, at % P], np.stack([s, m], -1).astype(np.float64))
         got = cache[0].cpu().numpy()[bt[0][at // P], :, at % P]
         assert np.array_equal(got, packed(n)), (rot, np.argwhere(got != packed(n))[:4].tolist())
+
+
+@pytest.mark.parametrize('D,Nq,H', [(64, 6, 3), (128, 32, 8), (256, 16, 2)])
+def test_rows_of_inactive_slots(D, Nq, H):
+    """Zero rows of inactive slots of any number of rows, alone and among others, long tables and short ones."""
+    for seqs, most, P in ((3, 700, 16), (40, 33, 20), (300, 5, 16)):
+        rng = np.random.default_rng(seqs)
+        for table in (1, 1000):                              # (pages of a short table, of one whose units are cut)
+            new = rng.integers(0, most, seqs).tolist()
+            lens = [n + int(rng.integers(0, 20)) if n and n < 9 and rng.random() < 0.5 else 0 for n in new]
+            new[0], lens[0] = 2, 17
+            bt, pages = tables(5, lens, P)
+            bt = np.concatenate([bt, np.zeros((seqs, max(0, table // P - bt.shape[1])), np.int64)], 1)
+            cache = filled(31, pages, H, P, D)
+            T, cu = sum(new), cuts(new)
+            q = rand(33, T, Nq, D)
+            o = torch.full((T + 3, Nq, D), float('nan'), dtype=BF, device='cuda')
+            y = gdn.paged_kv4_attn_decode(q, *cache, i32(bt.tolist()), i32(lens), cu_seqlens=i32(cu), o=o[:T])
+            gdn.check_device_error()
+            assert o[T:].isnan().all()
+            for s, n in enumerate(lens):
+                if n == 0:
+                    assert (y[cu[s]:cu[s + 1]] == 0).all(), s
+            live = [t for s, n in enumerate(lens) if n for t in range(cu[s], cu[s + 1])]
+            some = [s for s, n in enumerate(lens) if n][:20]
+            ref = kv4_reference(torch.cat([q[cu[s]:cu[s + 1]] for s in some]), cache, bt[some], cuts([new[s] for s in some]),
+                                [lens[s] for s in some], D ** -0.5, None)
+            close4(torch.cat([y[cu[s]:cu[s + 1]] for s in some]), ref)
+            assert y[live].isfinite().all()
+
+
+def test_a_large_inactive_slot_does_not_hold_the_call():
+    """The rest of a step's rows as one inactive slot, 4000 rows of 32 heads of 128 (33 MB): the whole grid clears them.  One
+    warp alone writes 256 bytes a step, 128,000 of them: milliseconds.  The limit is a hundred times what a fill takes."""
+    D, Nq, H, P, rest = 128, 32, 8, 16, 4000
+    lens = [40, 300, 0]
+    bt, pages = tables(6, lens, P)
+    cache = filled(41, pages, H, P, D)
+    q = rand(43, rest + 2, Nq, D)
+    args = (q, *cache, i32(bt.tolist()), i32(lens))
+    o = torch.empty_like(q)
+    run = lambda: gdn.paged_kv4_attn_decode(*args, cu_seqlens=i32([0, 1, 2, rest + 2]), o=o)  # noqa: E731
+    times = []
+    for _ in range(7):
+        run()
+        a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        a.record()
+        run()
+        b.record()
+        b.synchronize()
+        times.append(a.elapsed_time(b))
+    assert min(times) < 0.6, times
+    assert (o[2:] == 0).all() and o[:2].abs().sum() > 0
+    gdn.check_device_error()
