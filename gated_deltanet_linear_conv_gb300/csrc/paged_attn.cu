@@ -272,15 +272,12 @@ __device__ __noinline__ int next_seq(const PagedAttnArgs& a, int s, Seq* q) {
   }
   return a.num_seqs;
 }
-// The rows of a sequence with nothing to attend, by a warp.
-__device__ __noinline__ void zero_rows(const PagedAttnArgs& a, const Seq& q) {
-  const int64_t b = (int64_t)q.bos * a.Nq * a.D, e = b + (int64_t)q.n * a.Nq * a.D;
-  const float z[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 1
-  for (int64_t i = b + (threadIdx.x & 31) * 4; i < e; i += 128) {
-    if (a.out_bf16) store4(static_cast<bf16*>(a.o) + i, z);
-    else store4(static_cast<float*>(a.o) + i, z);
-  }
+// (Two sequences of 300 tokens beside an inactive slot of 64 and 512 rows of 32 heads of 128, us: by one warp 202 and 1520, by
+// the grid 15.4 and 15.6; without the slot 10.1.)
+template <int THREADS>
+__device__ __noinline__ void zero_slots(const PagedAttnArgs& a, int64_t row, int64_t* scratch) {
+  zero_many<THREADS>([&](int s) { return load_seq(a, s); }, a.num_seqs, row, a.o, threadIdx.x, scratch,
+                     [] { tc::named_sync(1, THREADS); });
 }
 
 // Four elements of (token t, head h) from d: the gate, and y = o * sigmoid(gate).
@@ -746,8 +743,14 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
   const int per = (a.num_seqs + C::THREADS - 1) / C::THREADS;
   const int s_lo = min(a.num_seqs, tid * per), s_hi = min(a.num_seqs, s_lo + per);
   int64_t sum = 0;
+  const int64_t row = (int64_t)a.Nq * (a.out_bf16 ? D / 8 : D / 4);                // 16-byte words of a token's output
+  bool many = false;                               // see zero_many
 #pragma unroll 1
-  for (int s = s_lo; s < s_hi; ++s) sum += seq_work<C>(p, load_seq(a, s));
+  for (int s = s_lo; s < s_hi; ++s) {
+    const Seq q = load_seq(a, s);
+    sum += seq_work<C>(p, q);
+    many = many || (q.len == 0 && q.n * row > kFewWords);
+  }
   int64_t inc = sum;
 #pragma unroll
   for (int off = 1; off < 32; off <<= 1) {
@@ -755,7 +758,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
     if (lane >= off) inc += v;
   }
   if (lane == 31) scan[warp] = inc;
-  __syncthreads();
+  many = __syncthreads_or(many);
   int64_t before = inc - sum, total = 0;
 #pragma unroll
   for (int w = 0; w <= C::CW; ++w) {
@@ -933,8 +936,9 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
 #pragma unroll 1
   for (int s = blockIdx.x * C::CW + warp; s < a.num_seqs; s += gridDim.x * C::CW) {
     const Seq q = load_seq(a, s, lane == 0 ? a.err : nullptr);
-    if (q.n > 0 && q.len == 0) zero_rows(a, q);
+    if (q.n > 0 && q.len == 0 && q.n * row <= kFewWords) zero_few(a.o, q.bos * row, q.n * row);
   }
+  if (many) zero_slots<C::CW * 32>(a, row, reinterpret_cast<int64_t*>(head + 784));
   const int tw = warp % C::TG;                     // which slices; warps tw + k TG share them
   // The slices go round the warps from stage to stage.  In float32 also where tiles are not full:
   // five slices of four tokens on four warps took 592 us for the case at SimtWarp (in tiles of
