@@ -11,9 +11,10 @@
 // that need them: half-words of four nibbles for its elements, transposed for the values.
 //
 // Bound: the cache's bytes at HBM rate, 9/16 of a byte per element.  At that rate an SM has 400 issue slots per 16 tokens
-// of a kv head of 128; this kernel needs about 300, so the arithmetic is kept at word granularity
+// of a kv head of 128; this kernel needs 313, so the arithmetic is kept at word granularity
 // throughout.  256 sequences of 512 to 8192, 8 kv heads of 128 (1.26 GB): 247 us, 5.1 TB/s, 75 % of the copy
-// rate (the copies alone 194 us, the arithmetic alone 200) at the 12 warps per SM that 167 registers leave.
+// rate (in an earlier form of the same time the copies alone 194 us, the arithmetic alone 200) at the 12 warps per SM that 167
+// registers leave.
 //
 // Rows: eight rows (a new token and query head each, all of one kv head) are an octet, the
 // narrow side of the products; keys are the 16-row side, so no row of a product is padding:
@@ -21,13 +22,14 @@
 // A unit is one pass over a sequence: (sequence, kv head, NT octets).
 //
 // Weights enter the second product in f16, w = 8 p_j s_jg / r with r, of a row and group, a power of two next to the
-// greatest p_j s_jg so far (2^-11 relative; a bf16 output rounds by 2^-8), so that a row depends on nothing that it does not
-// see and on no other row, and neither large nor small values leave f16's range; p itself, l = sum p and sum p m are
-// float32.  The running maximum and r are brought up to date only when a lane's weights of a row over that maximum, 2 or 4
+// greatest p_j s_jg so far (2^-11 relative; a bf16 output rounds by 2^-8), so that neither what a row does not see nor other rows
+// cost it digits, and neither large nor small values leave f16's range; p itself, l = sum p and sum p m are
+// float32.  (Bits do differ with the batch: by it go the cuts of units, and when a warp's rows are brought up to date.)
+// The running maximum and r are brought up to date only when a lane's weights of a row over that maximum, 2 or 4
 // tokens, sum to more than 2^7 or some w passes f16's range: most slices need no exchange between lanes and no
 // rescaling.  (One r for all rows took 1 % less, 4 % in two octets, and let rows with other numbers cost each other digits.)
 //
-// Work split as in the 16-bit kernel: all slices of 16 or 32 tokens of all units lie end to end (a gap of kUnitCost for a
+// Work split as in the 16-bit kernel: all slices of 16 or 32 tokens of all units lie end to end (a gap of COST for a
 // unit's start and join), and each CTA takes an equal range, computed on the device from kv_lens;
 // pieces of units that cross ranges go to the workspace, and a second kernel joins them in order.  With short
 // tables ranges end at unit borders and nothing is joined.  Inside a CTA four warps take the slices of a piece
@@ -46,15 +48,19 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 // Ranges end at unit borders with tables up to kAlignTokens, and up to kAlignMany where there are as many units as CTAs.  Whole
-// units against cut ones, us: one sequence of 1000, 16 heads over 2 of 256, 17.0 and 13.5, of 500 11.4 and 13.6; 256 of
-// 100 to 900, 32 heads over 8 of 128, 55 and 64; 32 of 500 to 2000 26.7 and 20.7.
+// units against cut ones, us: one sequence of 1000, 16 heads over 2 of 256, 15.6 and 13.6, of 500 10.8 and 13.3; 256 of
+// 100 to 900, 32 heads over 8 of 128, 53.2 and 54.5; 32 of 500 to 2000 26.3 and 21.7.
 constexpr int kAlignTokens = 512, kAlignMany = 1024;
-// A unit's start and join, in tokens.  160, 320 and 640, us: 256 sequences of 512 to 8192, 32 heads over 8 of 128, 259, 253 and
-// 259; one sequence of 2000, 16 over 2 of 256, 12.6, 13.6 and 17.8.  Two octets of 64-wide heads have cheap tokens beside
-// their start: 320 and 512, 16 x 5 tokens of 0 to 8192, 24 heads over 8 of 64, 29.9 and 25.4 (other lengths 25.1 and 24.0).
-constexpr int kUnitCost = 320, kTwoUnitCost = 512;
-// Tokens of a range at least, where units are cut.  96, 192 and 384, us: one sequence of 1000, 16 heads over 2 of 256, 13.5,
-// 14.1 and 18.3; of 8000, 32 over 8 of 128, 12.7, 13.0 and 14.4; 32 of 500 to 2000 20.6, 21.0 and 20.6.
+// A unit's start and join, in tokens, of one octet of rows (below) and of more, which have dearer starts and joins.  160, 320,
+// 512 and 640, us: 256 sequences of 512 to 8192, 32 heads over 8 of 128, 269, 260, 262 and 266; 32 of 500 to 2000 26.8, 22.5,
+// 23.0 and 23.0; one of 2000, 16 over 2 of 256, 11.5, 13.5, 15.0 and 15.5.  Two octets (24 heads over 8 of 64, 4 or 5 tokens):
+// 16 sequences of 0 to 8192 36.7, 28.0, 26.2 and 26.5; 64 of 1000 to 3000 39.8, 39.0, 38.2 and 38.7; 128 of 100 to 9000 150, 137,
+// 132 and 133; of 128-wide heads (32 over 8, 3 tokens) 16 of 0 to 8192 42.3, 37.2, 37.1 and 37.9, 64 of 1000 to 3000 66.4,
+// 63.6, 63.6 and 64.6.  Four of 64-wide ones (9 tokens): 16 of 0 to 8192 42.2, 38.8, 37.4 and 38.0; 64 of 1000 to 3000 67.9,
+// 65.0, 63.9 and 64.9.
+constexpr int kUnitCost = 320, kManyUnitCost = 512;
+// Tokens of a range at least, where units are cut.  96, 192 and 384, us: one sequence of 1000, 16 heads over 2 of 256, 13.6,
+// 14.3 and 18.6; of 8000, 32 over 8 of 128, 13.1, 13.7 and 15.1; 32 of 500 to 2000 21.5, 21.4 and 21.6.
 constexpr int kMinTokens = 96;
 constexpr int kMaxCtas = 1024;
 constexpr float kLog2e = 1.4426950408889634f;
@@ -70,16 +76,17 @@ struct Cfg {
   static constexpr int ROWS = 8 * NT;
   static constexpr int SIZE = NG * NT;             // 16 accumulators each
   static constexpr int OCC = SIZE <= 1 ? 4 : SIZE <= 2 ? 3 : 2;    // CTAs per SM, by the registers they want
-  // Blocks of 16 tokens in a slice, a warp's step.  1 and 2, us: 256 sequences as above 328 and 298; two octets of 64-wide heads,
-  // 16 x 5 tokens of 4096 25.2 and 24.1, 64 x 4 of 1000 to 3000 40.8 and 38.8 (of 128-wide ones the registers do not suffice).
+  // Blocks of 16 tokens in a slice, a warp's step: two where the registers suffice.  1 and 2, us: 256 sequences as above 293 and
+  // 260; 64 of 1000 to 9000, 24 heads over 8 of 64, 57.6 and 52.6; two octets of 64-wide heads, 16 x 5 tokens of 4096 26.7 and
+  // 24.7, 64 x 4 of 1000 to 3000 40.6 and 38.2.
   static constexpr int U = NT == 1 || SIZE == 2 ? 2 : 1;
   static constexpr int SLICE = 16 * U;
-  static constexpr int COST = (NT == 2 && SIZE == 2 ? kTwoUnitCost : kUnitCost) / SLICE;
+  static constexpr int COST = (NT > 1 ? kManyUnitCost : kUnitCost) / SLICE;
   static constexpr int KV = SLICE * D / 2;         // bytes of a slice's keys (or values)
   static constexpr int SC = SLICE * NG * 4;        // of their scales
   static constexpr int STAGE = 2 * (KV + SC);
-  // Slices in a warp's ring.  As many and one more, us: one sequence of 131072, 16 heads over 2 of 256, 24.7 and 25.4; 64 of
-  // 1000 to 9000, 24 over 8 of 64, 56.3 and 60.4; 64 x 9 tokens of 1000 to 3000 65.6 and 66.4; 256 sequences as above 246 and 245.
+  // Slices in a warp's ring.  As many and one more, us: one sequence of 131072, 16 heads over 2 of 256, 24.9 and 26.3; 64 x 9
+  // tokens of 1000 to 3000, 24 over 8 of 64, 65.1 and 65.8; 64 of 1000 to 9000 and 256 sequences as above no difference.
   static constexpr int STAGES = U == 2 ? 2 : 3;
   static constexpr int RING = kWarps * STAGES * STAGE;
   static constexpr int JP = D + 4;                 // join row pitch (floats)
@@ -845,8 +852,8 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, NT>::OCC)) kv4_attn_kernel(c
 // joined through shared memory in order.  PG = 1, about as many units as CTAs (about two pieces each): block (c, y)
 // joins the unit that starts in CTA c's range and ends behind it, if there is one.  PG > 1: blocks (u, y) join the
 // unit of the u-th CTA with a record.  BATCH pieces of a group are loaded at a time: for PG = 16, where a unit may have
-// hundreds, 4 and 10, us: one sequence of 131072, 16 heads over 2 of 256, 26.3 and 25.4; of 30000, 32 over 8 of 128, 19.8
-// and 16.1.  (2 x 3 tokens of 30000, 16 over 2 of 256, 29.1 and 31.0; 29.6 with PG = 4, which such 12 units get.)
+// hundreds, 4 and 10, us: one sequence of 131072, 16 heads over 2 of 256, 26.5 and 24.9 (33.2 with PG = 4); of 30000, 32 over 8
+// of 128, 16.7 and 16.1 (20.6 with PG = 4).
 constexpr int kJoinThreads = 256;
 template <int D, int COLS, int PG, int BATCH = 4>
 __global__ void __launch_bounds__(kJoinThreads) kv4_join_kernel(const __grid_constant__ Params p, int ctas, int rows) {
@@ -968,8 +975,8 @@ __global__ void __launch_bounds__(kJoinThreads) kv4_join_kernel(const __grid_con
 }
 
 // ------------------------------------------------------------------ host
-// Octets per pass at most: as many as registers hold the sums and queries of.  Twice as many, us: 16 x 4 tokens of 4096, 64 heads
-// over 8 of 128, 71 against 56 (spilled registers); 16 x 2, 32 over 4 of 256, 50 against 41.
+// Octets per pass at most: as many as registers hold the sums and queries of.  Twice as many, us (an earlier form of the kernel,
+// registers spilled): 16 x 4 tokens of 4096, 64 heads over 8 of 128, 71 against 56; 16 x 2, 32 over 4 of 256, 50 against 41.
 constexpr int most_octets(int D) { return D == 256 ? 1 : D == 128 ? 2 : 4; }
 constexpr int occupancy(int D, int nt) { return D / 64 * nt <= 1 ? 4 : D / 64 * nt <= 2 ? 3 : 2; }
 int grid_of(int D, int nt) { return std::min(occupancy(D, nt) * num_sms(), kMaxCtas); }

@@ -145,3 +145,23 @@ def test_a_large_inactive_slot_does_not_hold_the_call():
     assert min(times) < 0.6, times
     assert (o[2:] == 0).all() and o[:2].abs().sum() > 0
     gdn.check_device_error()
+
+
+@pytest.mark.parametrize('D,G', [(64, 3), (128, 8), (256, 8), (64, 16)])
+def test_a_sequence_alone_and_in_company(D, G):
+    """Cuts and sums go by the batch, so bits may differ with it; the row is right in each."""
+    P, H, new = 16, 2, [1, 2, 1, 3]
+    lens = [1500, 40, 700, 90]
+    bt, pages = tables(8, lens, P)
+    cache = filled(51, pages, H, P, D)
+    cache[3][bt[2][:3]] *= 2.0 ** 30                         # (a neighbour with other numbers)
+    cu = cuts(new)
+    q = rand(53, cu[-1], H * G, D)
+    y = gdn.paged_kv4_attn_decode(q, *cache, i32(bt.tolist()), i32(lens), cu_seqlens=i32(cu))
+    for s in range(4):
+        part = q[cu[s]:cu[s + 1]].contiguous()
+        ref = kv4_reference(part, cache, bt[s:s + 1], [0, new[s]], lens[s:s + 1], D ** -0.5, None)
+        alone = gdn.paged_kv4_attn_decode(part, *cache, i32(bt[s:s + 1].tolist()), i32(lens[s:s + 1]))
+        close4(alone, ref, ('alone', s))
+        close4(y[cu[s]:cu[s + 1]], ref, ('in company', s))
+    gdn.check_device_error()
