@@ -605,7 +605,7 @@ int gdn_paged_kv4_read(const gdn_attn_dims* dims, const int32_t* cu_seqlens,
  *              shared by calls that can run at the same time.  For the current device
  *              and tables of up to table_tokens = max_pages * page_size entries: 0
  *              for short tables, else the same for all numbers of sequences and tokens
- *              (20 MB at most on 152 SMs).
+ *              (5.2 MB at most on 152 SMs).
  * total_tokens * num_q_heads is below 2^31 (else GDN_ERR_UNSUPPORTED).
  * ------------------------------------------------------------------------ */
 int gdn_paged_kv4_attn_decode_workspace_size(const gdn_attn_dims* dims, int64_t table_tokens, size_t* bytes);
