@@ -41,7 +41,9 @@ __global__ void __launch_bounds__(kThreads) kv4_read_kernel(const __grid_constan
   constexpr int LPR = D / 8;                       // lanes per row
   const int c = threadIdx.x % LPR;
   const int64_t t64 = (int64_t)blockIdx.x * (kThreads / LPR) + threadIdx.x / LPR;
-  const int rows = 2 * p.Nkv, r_lo = blockIdx.y * span, r_hi = min(rows, r_lo + span);   // k heads, then v heads
+  // k heads, then v heads, of the outputs that are given
+  const int r_lo = (p.k_out == nullptr ? p.Nkv : 0) + blockIdx.y * span;
+  const int r_hi = min(p.v_out == nullptr ? p.Nkv : 2 * p.Nkv, r_lo + span);
   pdl_launch_next();
   pdl_wait();
   if (blockIdx.y == 0)
@@ -94,7 +96,6 @@ __global__ void __launch_bounds__(kThreads) kv4_read_kernel(const __grid_constan
       const int r = r0 + i, h = r < p.Nkv ? r : r - p.Nkv;
       if (r >= r_hi) break;
       T* out = static_cast<T*>(r < p.Nkv ? p.k_out : p.v_out);
-      if (out == nullptr) continue;
       float x[8];
       unpack(w[i], sm[i], x);
       store8(out + ((int64_t)t * p.Nkv + h) * D + c * 8, x);
@@ -104,7 +105,7 @@ __global__ void __launch_bounds__(kThreads) kv4_read_kernel(const __grid_constan
 
 template <typename T, int D>
 cudaError_t launch_d(const Kv4ReadArgs& p, cudaStream_t s) {
-  const int per_block = kThreads / (D / 8), rows = 2 * p.Nkv;
+  const int per_block = kThreads / (D / 8), rows = ((p.k_out != nullptr) + (p.v_out != nullptr)) * p.Nkv;
   const int64_t tblocks = ((int64_t)p.total + per_block - 1) / per_block;
   // rows of a token in one block, or split where the tokens alone do not fill the device
   const int64_t want = 8 * num_sms();

@@ -165,3 +165,25 @@ def test_a_sequence_alone_and_in_company(D, G):
         close4(alone, ref, ('alone', s))
         close4(y[cu[s]:cu[s + 1]], ref, ('in company', s))
     gdn.check_device_error()
+
+
+@pytest.mark.parametrize('D,H', [(64, 5), (128, 2), (256, 1)])
+@pytest.mark.parametrize('dtype', [BF, F32])
+def test_read_of_keys_or_values_alone(D, H, dtype):
+    """One output NULL: the other as with both, and nothing behind either."""
+    lens, P = [37, 1, 0, 800], 16
+    bt, pages = tables(9, lens, P)
+    cache, T, cu = filled(61, pages, H, P, D), sum(lens), i32(cuts(lens))
+    table, n = i32(bt.tolist()), i32(lens)
+    both = gdn.paged_kv4_read(*cache, table, n, T, cu_seqlens=cu, out_dtype=dtype)
+    st, ss = cache[0].stride(), cache[2].stride()
+    c = gdn.gdn_paged_cache4(*(t.data_ptr() for t in cache), st[0], st[1], st[2], ss[0], ss[1], ss[2], pages, P, bt.shape[1],
+                             table.data_ptr(), n.data_ptr())
+    for i in range(2):
+        out = torch.full((T + 2, H, D), -7.0, dtype=dtype, device='cuda')
+        at = [out.data_ptr() if i == j else None for j in range(2)]
+        assert gdn.lib().gdn_paged_kv4_read(gdn.gdn_attn_dims(len(lens), T, H, H, D), cu.data_ptr(), c, *at,
+                                            gdn.GDN_BF16 if dtype == BF else gdn.GDN_F32,
+                                            torch.cuda.current_stream().cuda_stream) == 0
+        gdn.check_device_error()
+        assert torch.equal(out[:T], both[i]) and (out[T:] == -7).all()
