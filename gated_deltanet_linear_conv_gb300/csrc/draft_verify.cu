@@ -313,8 +313,11 @@ __global__ void __launch_bounds__(kThreads, 4) draft_verify_kernel(const __grid_
 
 template <typename T>
 cudaError_t launch_t(const DraftVerifyArgs& p, cudaStream_t s) {
-  // CTAs per sequence: eight (a portable cluster) where the sequences alone do not fill the device.  1, 2, 4 and 8 for the 256
-  // sequences: 55, 41, 44 and 50 us.
+  // CTAs per sequence: eight (a portable cluster) where the sequences alone do not fill the device.  1, 2, 4 and 8, us, most
+  // drafts kept, the rule's choice in brackets: 512 x 2 drafts of 32000 in float32 [17.2], 20.2, 26.9 and 48.5; 256 x 4 of 131072
+  // 43.2, [27.6], 31.3 and 39.0, of 50256 in bf16 18.8, [13.1], 16.9 and 26.0; 128 x 4 of those 15.6, 13.0, [9.9] and 14.6; 100 x 4
+  // of 131072 in float32 30.7, 19.5, [16.2] and 19.6, 64 x 4 27.7, 20.0, 14.9 and [12.0], 16 x 4 26.4, 15.5, 10.3 and [8.8]; one of
+  // 32000 7.4, 5.6, 5.1 and [5.2].
   int ctas = 8;
   while (ctas > 1 && ((int64_t)p.num_seqs * ctas > 4 * num_sms() || ctas * kTile > p.vocab)) ctas /= 2;
   const int64_t unit = 16 / sizeof(T);

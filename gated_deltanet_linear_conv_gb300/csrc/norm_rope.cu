@@ -95,8 +95,8 @@ constexpr float kFloatMost = 3.40282347e38f;
 // steps of the larger.
 constexpr float kRowError = 0x1.6p-20f;            // 22 steps
 
-// x / s, correctly rounded but for results next to the smallest numbers (r = 1 / s): a quotient that is a half, where
-// the rounding turns, comes out as it is.
+// x / s by Markstein's correction of a quotient by its exact remainder (r = 1 / s), correctly rounded but for results next to
+// the smallest numbers: a quotient that is a half, where the rounding turns, comes out as it is.
 __device__ __forceinline__ float quotient(float x, float s, float r) {
   const float q = __fmul_rn(x, r);
   return __fmaf_rn(__fmaf_rn(-q, s, x), r, q);

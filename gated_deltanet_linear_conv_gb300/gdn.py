@@ -912,9 +912,10 @@ def paged_plan(new_lens, kv_lens, pages_held, free_ring, free_pages, block_table
 
 def draft_verify(target_probs, tokens, uniform, draft_probs=None, cu_seqlens=None, num_seqs=1, kv_lens=None, out=None):
     """gdn_draft_verify: target_probs [T, V] (bf16 or float32; rows may be apart), tokens [T] int32 and uniform [T]
-    float32 of a multi-token step, draft_probs [N, drafts, V] (any strides over the first two axes; [N, 0, V] only where
-    no sequence can have more than one row) or None.  Returns (accepted [N], out_tokens [T], kv_lens [N] less the refused
-    drafts, None without kv_lens); ``out`` may supply them (its kv_lens may be the input)."""
+    float32 of a multi-token step (a prompt's last token alone, with bounds that count it as one row), draft_probs [N,
+    drafts, V] (any strides over the first two axes; [N, 0, V] only where no sequence can have more than one row) or None.
+    Returns (accepted [N], out_tokens [T], kv_lens [N] less the refused drafts, None without kv_lens); ``out`` may supply
+    them (its kv_lens may be the input)."""
     T, V = target_probs.shape
     dev = _device(target_probs)
     if cu_seqlens is not None:

@@ -597,7 +597,9 @@ int gdn_paged_kv4_read(const gdn_attn_dims* dims, const int32_t* cu_seqlens,
  * past a token's own index.  Scores, softmax statistics and sums are float32; a
  * weight times a step enters the product with the numbers n in f16 (2^-11 relative to
  * sum_j p_j s_j n_j: an eighth of the rounding of a bf16 output; one below 2^-17 of the
- * row's largest p_j s_j in the group is off by up to 2^-27 of that).
+ * row's largest p_j s_j in the group is off by up to 2^-27 of that), and a query's elements
+ * too, next to a power of two of the row's own (off by up to 2^-31 of its largest).  A row's
+ * bits may differ with the other sequences of the call (the order of its sums does).
  *   q, gate    [tokens, Nq, D]   bf16 (strided); gate may be NULL
  *   o          [tokens, Nq, D]   bf16, contiguous
  *   workspace  device scratch of gdn_paged_kv4_attn_decode_workspace_size() bytes
@@ -638,7 +640,8 @@ int gdn_paged_kv4_attn_decode(const gdn_attn_dims* dims, const int32_t* cu_seqle
  *   block_table [N, max_pages], free_pages [num_pages]   updated in place
  *   cu_seqlens  [N + 1]         prefix sums of max(new_lens, 0)
  *   positions   [total_tokens]  each new token's cache index, or NULL
- *   slots       [total_tokens]  its page * page_size + slot, or NULL
+ *   slots       [total_tokens]  its page * page_size + slot, or NULL (for calls of the
+ *                               user's own; this library's go by the block table)
  *   kv_lens_out, pages_held_out, free_ring_out   the state after the step; each may
  *                               be its input.  Ended sequences have length 0.
  * total_tokens rows that the new tokens do not fill have position 0 and slot -1
@@ -685,7 +688,10 @@ int gdn_paged_plan(const gdn_page_plan* plan, void* stream);
  *
  * Sequence s has the n rows [bos, eos) of the step (cu_seqlens, or equally many):
  * tokens[bos] is certain, tokens[bos + 1 ..] are its n - 1 drafts, and row bos + i
- * of target_probs is the target's distribution behind token i.  Draft x = tokens[bos
+ * of target_probs is the target's distribution behind token i.  In a step that also
+ * has prompts these rows are fewer than gdn_paged_plan's: a prompt's last token alone
+ * (n = 1), whose probabilities are the only ones needed, so the call gets cu_seqlens of
+ * its own.  Draft x = tokens[bos
  * + i + 1] is kept while
  *   uniform[bos + i] * draft_probs[s, i, x] < target_probs[bos + i, x]   (in order)
  * with draft_probs counted as 1 at x where none are given (drafts that were looked
@@ -706,8 +712,10 @@ int gdn_paged_plan(const gdn_page_plan* plan, void* stream);
  *   out_tokens    [T] int32, not tokens itself: rows bos .. bos + a - 1 the drafts kept, bos + a the token
  *                 drawn, the others -1
  *   kv_lens, kv_lens_out  [N] int32 or both NULL: kv_lens_out = kv_lens - (n - 1 - a),
- *                 the cached tokens that stay; may be the same.  Length 0 marks an
- *                 inactive slot of a padded batch: a = 0, its out_tokens -1
+ *                 the cached tokens that stay; may be the same.  kv_lens counts the
+ *                 step's tokens (gdn_paged_plan's kv_lens_out); fewer than the refused
+ *                 ones give a length below 0, which gdn_paged_plan refuses.  Length 0 marks
+ *                 an inactive slot of a padded batch: a = 0, its out_tokens -1
  * A draft outside [0, V) or without a row of draft_probs is refused, and a row that
  * has no weight draws -1; both raise the device error flag.
  * V at most 2^21 (else GDN_ERR_UNSUPPORTED).

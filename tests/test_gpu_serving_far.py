@@ -3,6 +3,7 @@
 import pytest
 import torch
 
+import oracle.serving_oracle as S
 from gated_deltanet_linear_conv_gb300 import gdn
 
 pytestmark = pytest.mark.gpu
@@ -75,3 +76,32 @@ def test_plan_page_out_of_range_given_back(bad, seqs):
             gdn.check_device_error()
         assert out.free_ring.tolist() == [11, 2] and [int(free[11]), int(free[0])] == [3, bad if flagged else 4]
         assert out.pages_held.tolist()[0] == 0 and out.kv_lens.tolist()[0] == 0
+
+
+def test_a_step_of_prompts_and_drafts():
+    """Prompts beside sequences with drafts: the plan's bounds count every token, the verification's the rows with
+    probabilities, one of a prompt.  Lengths and the next step against the oracles."""
+    N, P, V, W = 5, 8, 200, 12
+    gen = torch.Generator().manual_seed(3)
+    pages = N * W
+    st = dict(lens=[0] * N, held=[0] * N, ring=[0, pages], free=torch.randperm(pages, generator=gen).tolist(), table=[[0] * W for _ in range(N)])
+    dev = {k: i32(v) for k, v in st.items()}
+    for new, prompt in (([20, 0, 9, 0, 1], {0, 2, 4}), ([4, 17, 4, 0, 3], {1}), ([4, 3, -1, 30, 1], {3}), ([2, 4, 5, 4, -1], {2})):
+        T = sum(max(n, 0) for n in new)
+        plan = gdn.paged_plan(i32(new), dev['lens'], dev['held'], dev['ring'], dev['free'], dev['table'], P, T)
+        ref = S.plan(new, page_size=P, total=T, **st)
+        assert plan.cu_seqlens.tolist() == ref['cu'] and plan.kv_lens.tolist() == ref['lens']
+        last = [list(range(a, b))[-1 if s in prompt else 0:] for s, (a, b) in enumerate(zip(ref['cu'], ref['cu'][1:]))]
+        rows = [t for r in last for t in r]
+        cu = [sum(map(len, last[:s])) for s in range(N + 1)]
+        p = torch.softmax(torch.randn(T, V, generator=gen) * 2, -1)[rows]
+        tok, u = torch.randint(V, (T,), generator=gen, dtype=torch.int32)[rows], torch.rand(T, generator=gen)[rows]
+        acc, out, lens = gdn.draft_verify(p.cuda(), tok.cuda(), u.cuda(), cu_seqlens=i32(cu), kv_lens=plan.kv_lens)
+        racc, rout, rlens = S.verify(p.double().numpy(), tok.tolist(), u.double().tolist(), None, cu, ref['lens'])
+        assert (acc.tolist(), out.tolist(), lens.tolist()) == (racc, rout, rlens)
+        for s in prompt:
+            assert acc[s] == 0 and out[cu[s]] >= 0 and rlens[s] == ref['lens'][s]          # all of a prompt stays
+        st = dict(lens=rlens, **{x: ref[x] for x in ('held', 'ring', 'free', 'table')})
+        dev.update(lens=lens, held=plan.pages_held, ring=plan.free_ring)
+        assert dev['table'].tolist() == ref['table']
+    gdn.check_device_error()
