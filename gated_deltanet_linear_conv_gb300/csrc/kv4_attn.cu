@@ -13,7 +13,7 @@
 // Bound: the cache's bytes at HBM rate, 9/16 of a byte per element.  At that rate an SM has 400 issue slots per 16 tokens
 // of a kv head of 128; this kernel needs 313, so the arithmetic is kept at word granularity
 // throughout.  256 sequences of 512 to 8192, 8 kv heads of 128 (1.26 GB): 247 us, 5.1 TB/s, 75 % of the copy
-// rate (in an earlier form of the same time the copies alone 194 us, the arithmetic alone 200) at the 12 warps per SM that 167
+// rate (in an earlier form of the same time the copies alone 194 us, the arithmetic alone 200) at the 12 warps per SM that 168
 // registers leave.
 //
 // Rows: eight rows (a new token and query head each, all of one kv head) are an octet, the
